@@ -1,6 +1,7 @@
 /*
- * mo.h - C ABI of the matrix-aware optimizer-step library (Muon, SOAP and
- * the Newton-Schulz orthogonaliser) for NVIDIA B200 (sm_100a).
+ * mo.h - C ABI of the matrix-aware optimizer-step library (Muon, SOAP, the
+ * Newton-Schulz orthogonaliser, and AdamW for what is not a matrix) for
+ * NVIDIA B200 (sm_100a).
  *
  * Conventions for every call below
  * --------------------------------
@@ -119,7 +120,8 @@ MO_API mo_status mo_device_status(mo_ctx* ctx, void* stream, int32_t* status);
  * 4 update P X, 5 apply / store, 6 SOAP elementwise, 7 SOAP rotations, 8 SOAP
  * power step and QR (other), 9 mo_gemm_bf16, 10 SOAP factor EMAs, 11 QR
  * diagonal Cholesky blocks, 12 QR row-block solves, 13 QR trailing updates,
- * 14 fused small-matrix Newton-Schulz / Muon. */
+ * 14 fused small-matrix Newton-Schulz / Muon, 15 pointer tables, 16 AdamW
+ * steps, 17 8-bit moments (pack, unpack), 18 gradient clipping. */
 MO_API mo_status mo_profile_enable(mo_ctx* ctx, int enable);
 MO_API mo_status mo_profile_read(mo_ctx* ctx, double* ms, double* flops, int64_t* launches, int nkinds);
 
@@ -339,6 +341,164 @@ MO_API mo_status soap_muon_step(mo_ctx* ctx, const mo_soap_muon_mat* mats /* hos
 /* Exact workspace of soap_muon_step for these matrices (sides as given). */
 MO_API mo_status mo_soap_muon_workspace_bytes(mo_ctx* ctx, const mo_soap_muon_mat* mats, int n,
                                               size_t* bytes);
+
+/* ------------------------------------------------------------------ AdamW
+ * One AdamW step over a list of tensors of any shapes, for what a model holds
+ * beside its matrices (embeddings, output heads, norms, biases; "LLM
+ * Optimizers: From SGD and AdamW to SOAP, Muon, and Scalable Training",
+ * sections 5 and 6; the routing rule is its section 11.5):
+ *   g <- s G                           (s = *grad_scale, 1 when NULL)
+ *   M <- b1 M + (1 - b1) g
+ *   V <- b2 V + (1 - b2) g * g
+ *   W <- (1 - lr' wd) W - lr' (M / (1 - b1^t)) / (sqrt(V / (1 - b2^t)) + eps)
+ * with lr' = lr * lr_scale and wd = weight_decay of the tensor.  The whole list
+ * takes one launch for each 320 tensors and no workspace.
+ *  - A tensor is numel contiguous elements at a pointer aligned to its
+ *    element; numel 0 or G == NULL skips it.  The wide path needs pointers
+ *    aligned to 8 elements (8-bit codes to 8 bytes) and gives the same bits.
+ *  - W is fp32 or bf16, G fp32, bf16 or fp16, in any mix over the list.  fp32 W
+ *    may have a copy in bf16 or fp16, which receives the new W rounded to
+ *    nearest.
+ *  - The moments are formed in fp32 as rn(rn(b1 M) + rn((1 - b1) g)) and
+ *    rn(rn(b2 V) + rn((1 - b2) rn(g g))), the constants rounded to fp32 from
+ *    the doubles of the config.
+ *  - bf16 W is rounded to nearest, or with stochastic != 0 to the neighbour
+ *    above with the probability of its distance, so that updates below half a
+ *    step are not lost.  The random bits are a function of (seed, step, place
+ *    in the list, element) alone.
+ *  - step_dev, lr_dev: the step and learning rate are read on the device when
+ *    the kernel runs (a captured step replayed with a new step and rate);
+ *    they replace `step` and cfg->lr.  *step_dev must be >= 1.
+ *  - skip: when *skip != 0 the call changes nothing (e.g. the nonfinite flag of
+ *    clip_grads).
+ *  - Buffers that a call writes must not overlap any other buffer of the call;
+ *    such a list is refused. */
+typedef enum { MO_F32 = 0, MO_BF16 = 1, MO_F16 = 2 } mo_type;
+
+typedef struct {
+  int64_t numel;
+  void* W;              /* parameter, updated in place */
+  const void* G;        /* gradient; NULL skips this tensor */
+  float* M;             /* first moment (zero before the first step) */
+  float* V;             /* second moment (zero before the first step) */
+  void* copy;           /* optional low-precision copy of W, or NULL */
+  int w_type, g_type, copy_type;   /* mo_type */
+  float lr_scale;       /* factor of lr (1) */
+  float weight_decay;   /* >= 0 */
+} mo_adamw_tensor;
+
+typedef struct {
+  double lr, beta1, beta2, eps;    /* lr >= 0, 0 <= beta < 1, eps >= 0 */
+  int bias_correction;             /* 1: divide by 1 - beta^t (default) */
+  int stochastic;                  /* 1: stochastic rounding (bf16 W, 8-bit V) */
+  uint64_t seed;
+  const float* lr_dev;             /* optional device scalars */
+  const int64_t* step_dev;
+  const float* grad_scale;
+  const int32_t* skip;
+} mo_adamw_cfg;
+
+MO_API mo_status adamw_step(mo_ctx* ctx, const mo_adamw_tensor* list /* host array */, int n,
+                            const mo_adamw_cfg* cfg, int64_t step, void* stream);
+
+/* ------------------------------------------------------------------ AdamW, 8-bit moments
+ * The same step with both moments held in 8 bits.  Each block of 256 elements,
+ * counted from the tensor's start, shares one scale byte s for each moment,
+ * which stands for 2^(s - 127):
+ *   M8  e4m3 codes, MS = max(1, E(max |M|) - 7)
+ *   V8  unsigned floats with 5 exponent bits (bias 15) and 3 mantissa bits,
+ *       VS = max(1, E(max V) - 15); code 255 stands for a value that is not
+ *       finite; a V above 0 never gets code 0
+ * with E the biased exponent of the block's largest finite fp32 magnitude.  The
+ * scales are powers of two, so the codes of an unchanged block stay what they
+ * are.  An infinite first moment becomes a NaN, which e4m3 has.  W is computed
+ * from the new moments before they are rounded to codes.  M is rounded to
+ * nearest-even; V to nearest-even or, with stochastic != 0, up with the
+ * probability of its distance: with b2 = 0.999 V moves by 0.1 % of itself in a
+ * step and half a step of its code is 3 to 6 %, so that nearest rounding would
+ * leave a slowly changing V where it is.  All zero codes and scales are the
+ * zero moments of the first step.  M8 and V8 hold numel bytes, MS and VS
+ * ceil(numel / 256).  Everything else is as in adamw_step. */
+typedef struct {
+  int64_t numel;
+  void* W;
+  const void* G;        /* NULL skips this tensor */
+  uint8_t* M8;
+  uint8_t* V8;
+  uint8_t* MS;
+  uint8_t* VS;
+  void* copy;
+  int w_type, g_type, copy_type;
+  float lr_scale;
+  float weight_decay;
+} mo_adamw8_tensor;
+
+MO_API mo_status adamw8_step(mo_ctx* ctx, const mo_adamw8_tensor* list /* host array */, int n,
+                             const mo_adamw_cfg* cfg, int64_t step, void* stream);
+
+/* Conversion between moments in fp32 or bf16 and 8 bits (checkpoints, a run
+ * that changes its kind of state).  pack writes the codes of M and V, rounded
+ * as adamw8_step does; a negative V takes code 0.  unpack writes the values
+ * that codes stand for, exact in fp32 and in bf16 down to their subnormals. */
+typedef struct {
+  int64_t numel;
+  uint8_t* M8;
+  uint8_t* V8;
+  uint8_t* MS;
+  uint8_t* VS;
+  void* M;
+  void* V;
+  int type;             /* of M and V: MO_F32 or MO_BF16 */
+} mo_adamw8_moments;
+
+typedef struct {
+  int stochastic;       /* of V, from (seed, step, place in the list, element) */
+  uint64_t seed;
+  int64_t step;
+  const int64_t* step_dev;   /* optional; replaces step */
+} mo_pack_cfg;
+
+MO_API mo_status adamw8_pack(mo_ctx* ctx, const mo_adamw8_moments* list, int n, const mo_pack_cfg* cfg,
+                             void* stream);
+MO_API mo_status adamw8_unpack(mo_ctx* ctx, const mo_adamw8_moments* list, int n, void* stream);
+
+/* ------------------------------------------------------------------ gradient clipping
+ * The 2-norm of all gradients of a list together and the factor that brings it
+ * to max_norm at most ("LLM Optimizers", sections 7.4 and 7.5):
+ *   norm   = || s G ||             (s = *scale, 1 when NULL)
+ *   factor = s min(1, max_norm / (norm + 1e-6))
+ * With apply != 0 out_i = factor G_i, rounded to nearest in out's type; out == NULL
+ * (or out == G) scales G_i in place.  With an out in fp32, 16-bit gradients
+ * become the fp32 matrices that muon_step and soap_step take.  With apply == 0
+ * only norm and factor are written; adamw_step takes the factor as grad_scale.
+ *  - Squares are taken in fp32, summed eight at a time in fp32 and from there
+ *    on in fp64, in an order that the list and the number of SMs fix.
+ *  - Nothing is special about a norm that is not finite (the factor is then 0
+ *    or a NaN); *nonfinite tells it, for adamw_step's skip.
+ *  - The partial sums are in the attached workspace (MO_CLIP_WORKSPACE_BYTES
+ *    at least): like other calls that use it, calls must not overlap on the
+ *    GPU while they share one workspace.
+ *  - An empty list has norm 0. */
+#define MO_CLIP_WORKSPACE_BYTES (256u + 8u * 8192u)
+
+typedef struct {
+  int64_t numel;
+  const void* G;        /* NULL skips this tensor; written when scaled in place */
+  void* out;            /* NULL: in place */
+  int g_type, out_type;
+} mo_grad;
+
+typedef struct {
+  float max_norm;       /* >= 0; infinity: norm alone */
+  int apply;
+  const float* scale;   /* optional device scalar */
+  float* norm;          /* device scalars, written */
+  float* factor;
+  int32_t* nonfinite;   /* optional: 1 when the norm is not finite, else 0 */
+} mo_clip_cfg;
+
+MO_API mo_status clip_grads(mo_ctx* ctx, const mo_grad* list /* host array */, int n, const mo_clip_cfg* cfg,
+                            void* stream);
 
 /* ------------------------------------------------------------------ building block
  * The batched tensor-core GEMM the steps are built from, exposed for tests

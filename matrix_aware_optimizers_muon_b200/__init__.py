@@ -1,4 +1,5 @@
-"""Matrix-aware optimizer steps (Muon, SOAP, Newton-Schulz) on NVIDIA B200.
+"""Matrix-aware optimizer steps (Muon, SOAP, Newton-Schulz) on NVIDIA B200,
+with AdamW for a model's other tensors and clipping over all gradients.
 
 A thin Python binding of the C ABI in ``include/mo.h``: it turns torch
 tensors into device pointers and the current CUDA stream into a handle, and
@@ -11,10 +12,10 @@ import ctypes
 from ctypes import byref, c_int32, c_int64, c_size_t, c_void_p
 
 from . import _lib
-from ._lib import (GemmDesc, MuonCfg, MuonMat, NsCfg, SoapCfg, SoapMat, SoapMuonCfg, SoapMuonMat,
-                   OP_MUON, OP_NS, OP_SOAP)
+from ._lib import (AdamW8Moments, AdamW8Tensor, AdamWCfg, AdamWTensor, ClipCfg, GemmDesc, Grad, MuonCfg, MuonMat,
+                   NsCfg, PackCfg, SoapCfg, SoapMat, SoapMuonCfg, SoapMuonMat, OP_MUON, OP_NS, OP_SOAP)
 
-__all__ = ["Context", "MoError", "QUINTIC", "OP_MUON", "OP_SOAP", "OP_NS"]
+__all__ = ["Context", "MoError", "TensorList", "QUINTIC", "OP_MUON", "OP_SOAP", "OP_NS"]
 
 QUINTIC = (3.4445, -4.7750, 2.0315)
 
@@ -67,6 +68,50 @@ def _check_extent(t, name, rows, cols, ld, stride, batch, dtypes):
     if rows > 0 and cols > 0 and last > t.numel():
         raise ValueError(f"{name}: the {batch} x {rows} x {cols} operand (ld {ld}, stride {stride}) "
                          f"needs {last} elements, the tensor has {t.numel()}")
+
+
+def _type(t, name, i, device, types):
+    """The library's type of a flat tensor, checked: the library gets pointers only."""
+    import torch
+    codes = {torch.float32: _lib.F32, torch.bfloat16: _lib.BF16, torch.float16: _lib.F16, torch.uint8: None}
+    allowed = [{"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16, "u8": torch.uint8}[k]
+               for k in types]
+    if t.dtype not in allowed or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"tensor {i}: {name} must be a contiguous CUDA tensor of dtype {allowed}")
+    if t.device.index != device:
+        raise ValueError(f"tensor {i}: {name} is on {t.device}, the context on cuda:{device}")
+    return codes[t.dtype]
+
+
+def _same_numel(t, name, i, numel):
+    if t.numel() != numel:
+        raise ValueError(f"tensor {i}: {name} must have {numel} elements, it has {t.numel()}")
+
+
+def _scalar(t, name, device, dtype):
+    """Device pointer of a one-element tensor (None passes through)."""
+    if t is None:
+        return None
+    if t.dtype != dtype or not t.is_cuda or t.numel() != 1:
+        raise ValueError(f"{name} must be a one-element {dtype} CUDA tensor")
+    if t.device.index != device:
+        raise ValueError(f"{name} is on {t.device}, the context on cuda:{device}")
+    return t.data_ptr()
+
+
+class TensorList:
+    """A checked list for adamw_step, adamw8_step, adamw8_pack / adamw8_unpack or clip_grads.
+
+    A program that keeps its parameters, gradients and state in place makes
+    it once and passes it to every step; it holds the tensors.  Made by
+    Context.adamw_tensors, adamw8_tensors, adamw8_moments and clip_tensors."""
+
+    def __init__(self, kind, array, n, tensors, device):
+        self.kind, self.array, self.n, self.device = kind, array, n, device
+        self.tensors = tensors
+
+    def __len__(self):
+        return self.n
 
 
 class Context:
@@ -336,6 +381,170 @@ class Context:
                           modes[adjust_lr], damping, _ptr(nonfinite), 0 if refresh else 1)
         self._check(self.lib.soap_muon_step(self.handle, arr, n, byref(cfg), int(step),
                                             self._stream(stream)))
+
+    # ------------------------------------------------------------ AdamW, clipping
+    def _list(self, kind, mats):
+        """mats as a TensorList of this kind."""
+        if not isinstance(mats, TensorList):
+            return {"adamw": self.adamw_tensors, "adamw8": self.adamw8_tensors,
+                    "moments": self.adamw8_moments, "grads": self.clip_tensors}[kind](mats)
+        if mats.kind != kind or mats.device != self.device:
+            raise ValueError(f"a list for {kind!r} on cuda:{self.device} is needed, "
+                             f"this one is for {mats.kind!r} on cuda:{mats.device}")
+        return mats
+
+    def _step_fields(self, i, d, state, keep):
+        """What both kinds of AdamW tensors share: (numel, pointers, types, lr_scale, weight_decay)."""
+        W, G, copy = d["W"], d.get("G"), d.get("copy")
+        n = W.numel()
+        wt = _type(W, "W", i, self.device, ("f32", "bf16"))
+        gt = ct = _lib.F32
+        if G is not None:
+            gt = _type(G, "G", i, self.device, ("f32", "bf16", "f16"))
+            _same_numel(G, "G", i, n)
+        if copy is not None:
+            ct = _type(copy, "copy", i, self.device, ("bf16", "f16"))
+            _same_numel(copy, "copy", i, n)
+        keep.append((W, G, copy, *state))
+        return n, W, G, copy, wt, gt, ct, d.get("lr_scale", 1.0), d.get("weight_decay", 0.0)
+
+    def adamw_tensors(self, mats):
+        """The list for adamw_step: dicts with W, G (None: skipped), M, V (fp32)
+        and optionally copy, lr_scale (1) and weight_decay (0)."""
+        arr, keep = (AdamWTensor * max(len(mats), 1))(), []
+        for i, d in enumerate(mats):
+            M, V = d["M"], d["V"]
+            n, W, G, copy, wt, gt, ct, ls, wd = self._step_fields(i, d, (M, V), keep)
+            for t, nm in ((M, "M"), (V, "V")):
+                _type(t, nm, i, self.device, ("f32",))
+                _same_numel(t, nm, i, n)
+            arr[i] = AdamWTensor(n, _ptr(W), _ptr(G), _ptr(M), _ptr(V), _ptr(copy), wt, gt, ct, ls, wd)
+        return TensorList("adamw", arr, len(mats), keep, self.device)
+
+    def _codes(self, i, d, n):
+        codes = [d[k] for k in ("M8", "V8", "MS", "VS")]
+        for t, nm, size in zip(codes, ("M8", "V8", "MS", "VS"), (n, n, -(-n // 256), -(-n // 256))):
+            _type(t, nm, i, self.device, ("u8",))
+            _same_numel(t, nm, i, size)
+        return codes
+
+    def adamw8_tensors(self, mats):
+        """The list for adamw8_step: as adamw_tensors with the moments' codes
+        M8, V8 (uint8, one for each element) and scales MS, VS (uint8, one for
+        each 256 elements) in the place of M and V."""
+        arr, keep = (AdamW8Tensor * max(len(mats), 1))(), []
+        for i, d in enumerate(mats):
+            codes = self._codes(i, d, d["W"].numel())
+            n, W, G, copy, wt, gt, ct, ls, wd = self._step_fields(i, d, codes, keep)
+            arr[i] = AdamW8Tensor(n, _ptr(W), _ptr(G), *map(_ptr, codes), _ptr(copy), wt, gt, ct, ls, wd)
+        return TensorList("adamw8", arr, len(mats), keep, self.device)
+
+    def adamw8_state(self, W):
+        """Zero 8-bit moments for the parameter W: a dict of M8, V8, MS and VS."""
+        import torch
+        n = W.numel()
+        sizes = dict(M8=n, V8=n, MS=-(-n // 256), VS=-(-n // 256))
+        return {k: torch.zeros(s, dtype=torch.uint8, device=W.device) for k, s in sizes.items()}
+
+    def adamw8_moments(self, mats):
+        """The list for adamw8_pack and adamw8_unpack: dicts with M8, V8, MS, VS
+        and the moments M, V, both fp32 or both bf16."""
+        arr, keep = (AdamW8Moments * max(len(mats), 1))(), []
+        for i, d in enumerate(mats):
+            M, V = d["M"], d["V"]
+            n = M.numel()
+            types = [_type(t, nm, i, self.device, ("f32", "bf16")) for t, nm in ((M, "M"), (V, "V"))]
+            _same_numel(V, "V", i, n)
+            if types[0] != types[1]:
+                raise ValueError(f"tensor {i}: M and V must have one dtype")
+            codes = self._codes(i, d, n)
+            keep.append((M, V, *codes))
+            arr[i] = AdamW8Moments(n, *map(_ptr, codes), _ptr(M), _ptr(V), types[0])
+        return TensorList("moments", arr, len(mats), keep, self.device)
+
+    def clip_tensors(self, grads):
+        """The list for clip_grads: gradients, or dicts with G and out (None:
+        scaled in place); a gradient that is None is skipped."""
+        arr, keep = (Grad * max(len(grads), 1))(), []
+        types = ("f32", "bf16", "f16")
+        for i, d in enumerate(grads):
+            G, out = (d["G"], d.get("out")) if isinstance(d, dict) else (d, None)
+            if G is None:
+                continue
+            gt = ot = _type(G, "G", i, self.device, types)
+            if out is not None:
+                ot = _type(out, "out", i, self.device, types)
+                _same_numel(out, "out", i, G.numel())
+            keep.append((G, out))
+            arr[i] = Grad(G.numel(), _ptr(G), _ptr(out), gt, ot)
+        return TensorList("grads", arr, len(grads), keep, self.device)
+
+    def _adamw(self, fn, mats, step, lr, beta1, beta2, eps, bias_correction, grad_scale, skip, seed, stream):
+        import torch
+        step_dev = lr_dev = None
+        if isinstance(step, torch.Tensor):
+            step, step_dev = 1, _scalar(step, "step", self.device, torch.int64)
+        if isinstance(lr, torch.Tensor):
+            lr, lr_dev = 0.0, _scalar(lr, "lr", self.device, torch.float32)
+        cfg = AdamWCfg(lr, beta1, beta2, eps, int(bias_correction), int(seed is not None), seed or 0, lr_dev, step_dev,
+                       _scalar(grad_scale, "grad_scale", self.device, torch.float32),
+                       _scalar(skip, "skip", self.device, torch.int32))
+        self._check(fn(self.handle, mats.array, mats.n, byref(cfg), int(step), self._stream(stream)))
+
+    def adamw_step(self, mats, step, *, lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, bias_correction=True,
+                   grad_scale=None, skip=None, seed=None, stream=None):
+        """One AdamW step on a list of tensors (adamw_tensors, or what it takes).
+
+        ``step`` and ``lr`` are numbers, or one-element int64 / fp32 CUDA tensors
+        read when the kernel runs.  ``grad_scale`` (fp32) multiplies every
+        gradient, a nonzero ``skip`` (int32) leaves everything as it is.  With a
+        ``seed`` bf16 weights are rounded stochastically, else to nearest."""
+        self._adamw(self.lib.adamw_step, self._list("adamw", mats), step, lr, beta1, beta2, eps, bias_correction,
+                    grad_scale, skip, seed, stream)
+
+    def adamw8_step(self, mats, step, *, lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, bias_correction=True,
+                    grad_scale=None, skip=None, seed=0, stream=None):
+        """One AdamW step with both moments in 8 bits (adamw8_tensors, or what
+        it takes).  With a ``seed`` the second moment and bf16 weights are
+        rounded stochastically; None rounds to nearest, which leaves a slowly
+        changing second moment where it is.  The rest is as in adamw_step."""
+        self._adamw(self.lib.adamw8_step, self._list("adamw8", mats), step, lr, beta1, beta2, eps, bias_correction,
+                    grad_scale, skip, seed, stream)
+
+    def adamw8_pack(self, mats, *, seed=None, step=0, stream=None):
+        """Moments M, V to 8-bit codes (adamw8_moments, or what it takes); with a
+        ``seed`` V is rounded stochastically, with the bits of ``step``."""
+        import torch
+        mats = self._list("moments", mats)
+        step_dev = None
+        if isinstance(step, torch.Tensor):
+            step, step_dev = 0, _scalar(step, "step", self.device, torch.int64)
+        cfg = PackCfg(int(seed is not None), seed or 0, int(step), step_dev)
+        self._check(self.lib.adamw8_pack(self.handle, mats.array, mats.n, byref(cfg), self._stream(stream)))
+
+    def adamw8_unpack(self, mats, *, stream=None):
+        """The values that 8-bit codes stand for, written to M and V."""
+        mats = self._list("moments", mats)
+        self._check(self.lib.adamw8_unpack(self.handle, mats.array, mats.n, self._stream(stream)))
+
+    def clip_grads(self, grads, max_norm, *, apply=True, scale=None, nonfinite=None, stream=None, reserve=True):
+        """Scales the gradients of a list (clip_tensors, or what it takes) so that
+        their common 2-norm is at most ``max_norm``; returns (norm, factor) as
+        fp32 device scalars.  ``apply=False`` computes these alone (adamw_step
+        takes the factor as grad_scale).  ``scale`` (fp32 device scalar)
+        multiplies the gradients first; ``nonfinite`` (int32 device scalar)
+        receives 1 when the norm is not finite."""
+        import torch
+        grads = self._list("grads", grads)
+        if reserve and (self.workspace is None or self.workspace.numel() < _lib.CLIP_WORKSPACE_BYTES):
+            self.attach_workspace(_lib.CLIP_WORKSPACE_BYTES, stream)
+        with torch.cuda.stream(stream):     # the scalars belong to the stream that writes them
+            out = torch.empty(2, dtype=torch.float32, device=f"cuda:{self.device}")
+        norm, factor = out[0], out[1]
+        cfg = ClipCfg(max_norm, int(apply), _scalar(scale, "scale", self.device, torch.float32), norm.data_ptr(),
+                      factor.data_ptr(), _scalar(nonfinite, "nonfinite", self.device, torch.int32))
+        self._check(self.lib.clip_grads(self.handle, grads.array, grads.n, byref(cfg), self._stream(stream)))
+        return norm, factor
 
     def gemm_bf16(self, A, B, D, *, M, N, K, batch=1, a_mn=False, b_mn=False, sym=False,
                   alpha=1.0, beta=0.0, C=None, scale=None, alpha_pow=0, beta_pow=0,

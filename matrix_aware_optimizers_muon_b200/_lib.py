@@ -6,7 +6,8 @@ Loading fails loudly when ``libmo.so`` is missing; there is no fallback.
 
 import ctypes
 import os
-from ctypes import POINTER, c_char_p, c_float, c_int, c_int32, c_int64, c_size_t, c_void_p
+from ctypes import (POINTER, c_char_p, c_double, c_float, c_int, c_int32, c_int64, c_size_t, c_uint64,
+                    c_void_p)
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libmo.so")
@@ -22,7 +23,8 @@ OP_MUON, OP_SOAP, OP_NS = 0, 1, 2
 
 # kernel kinds reported by mo_profile_read
 KINDS = ["prep", "norm", "gram", "poly", "update", "apply", "soap_ew", "soap_rot", "soap_qr", "gemm",
-         "soap_ema", "qr_chol", "qr_rowblock", "qr_trail", "ns_small", "tables"]
+         "soap_ema", "qr_chol", "qr_rowblock", "qr_trail", "ns_small", "tables", "adamw", "moments",
+         "clip"]
 
 
 class MuonMat(ctypes.Structure):
@@ -81,6 +83,51 @@ class GemmDesc(ctypes.Structure):
                 ("band", c_int)]
 
 
+# element types of the AdamW and clipping calls
+F32, BF16, F16 = 0, 1, 2
+
+
+class AdamWTensor(ctypes.Structure):
+    _fields_ = [("numel", c_int64), ("W", c_void_p), ("G", c_void_p), ("M", c_void_p), ("V", c_void_p),
+                ("copy", c_void_p), ("w_type", c_int), ("g_type", c_int), ("copy_type", c_int),
+                ("lr_scale", c_float), ("weight_decay", c_float)]
+
+
+class AdamW8Tensor(ctypes.Structure):
+    _fields_ = [("numel", c_int64), ("W", c_void_p), ("G", c_void_p), ("M8", c_void_p), ("V8", c_void_p),
+                ("MS", c_void_p), ("VS", c_void_p), ("copy", c_void_p), ("w_type", c_int),
+                ("g_type", c_int), ("copy_type", c_int), ("lr_scale", c_float), ("weight_decay", c_float)]
+
+
+class AdamWCfg(ctypes.Structure):
+    _fields_ = [("lr", c_double), ("beta1", c_double), ("beta2", c_double), ("eps", c_double),
+                ("bias_correction", c_int), ("stochastic", c_int), ("seed", c_uint64),
+                ("lr_dev", c_void_p), ("step_dev", c_void_p), ("grad_scale", c_void_p),
+                ("skip", c_void_p)]
+
+
+class AdamW8Moments(ctypes.Structure):
+    _fields_ = [("numel", c_int64), ("M8", c_void_p), ("V8", c_void_p), ("MS", c_void_p),
+                ("VS", c_void_p), ("M", c_void_p), ("V", c_void_p), ("type", c_int)]
+
+
+class PackCfg(ctypes.Structure):
+    _fields_ = [("stochastic", c_int), ("seed", c_uint64), ("step", c_int64), ("step_dev", c_void_p)]
+
+
+class Grad(ctypes.Structure):
+    _fields_ = [("numel", c_int64), ("G", c_void_p), ("out", c_void_p), ("g_type", c_int),
+                ("out_type", c_int)]
+
+
+class ClipCfg(ctypes.Structure):
+    _fields_ = [("max_norm", c_float), ("apply", c_int), ("scale", c_void_p), ("norm", c_void_p),
+                ("factor", c_void_p), ("nonfinite", c_void_p)]
+
+
+CLIP_WORKSPACE_BYTES = 256 + 8 * 8192
+
+
 # name -> (restype, argtypes); every entry point declared in include/mo.h
 SIGNATURES = {
     "mo_ctx_create": (c_int, [POINTER(c_void_p), c_int]),
@@ -107,6 +154,11 @@ SIGNATURES = {
                                          c_int, POINTER(NsCfg), c_void_p]),
     "muon_step_strided": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_int64, c_int64, c_int,
                                   POINTER(MuonCfg), c_void_p]),
+    "adamw_step": (c_int, [c_void_p, POINTER(AdamWTensor), c_int, POINTER(AdamWCfg), c_int64, c_void_p]),
+    "adamw8_step": (c_int, [c_void_p, POINTER(AdamW8Tensor), c_int, POINTER(AdamWCfg), c_int64, c_void_p]),
+    "adamw8_pack": (c_int, [c_void_p, POINTER(AdamW8Moments), c_int, POINTER(PackCfg), c_void_p]),
+    "adamw8_unpack": (c_int, [c_void_p, POINTER(AdamW8Moments), c_int, c_void_p]),
+    "clip_grads": (c_int, [c_void_p, POINTER(Grad), c_int, POINTER(ClipCfg), c_void_p]),
     "mo_profile_enable": (c_int, [c_void_p, c_int]),
     "mo_profile_read": (c_int, [c_void_p, POINTER(ctypes.c_double), POINTER(ctypes.c_double),
                                 POINTER(c_int64), c_int]),

@@ -1,0 +1,83 @@
+// AdamW over lists of tensors (fp32 or 8-bit moments), the conversion of the
+// moments, and clipping by the global gradient norm: launch tables shared by
+// the entry points (adamw_api.cu) and the kernels (adamw.cu).
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+#include <cuda_runtime.h>
+
+namespace mo {
+
+constexpr int AW_BLOCK = 256;      // elements that share a scale of the 8-bit moments
+constexpr int AW_THREADS = 256;    // 8 warps, one 256-element block each
+constexpr int AW_CHUNK = AW_BLOCK * (AW_THREADS / 32);   // elements of one CTA pass
+constexpr int AW_MAX = 320;        // tensors per launch (the table travels in the kernel's parameters)
+
+enum AwType : unsigned char { AW_F32 = 0, AW_BF16 = 1, AW_F16 = 2, AW_NONE = 3 };
+
+// One tensor.  Which pointers are used depends on the kernel:
+//   adamw    W, G, M, V (fp32), C (optional low-precision copy of W)
+//   adamw8   W, G, M, V (codes), MS, VS (scales), C
+//   pack     G = first moment, C = second moment (read), M, V, MS, VS (written)
+//   unpack   M, V, MS, VS (read), W = first moment, C = second moment (written)
+//   norm     G;  scale: G, C = output
+struct AwTensor {
+  void* W;
+  const void* G;
+  void* M;
+  void* V;
+  void* C;
+  unsigned char* MS;
+  unsigned char* VS;
+  long long numel;
+  float lr_scale, wd;
+  unsigned index;                  // place in the caller's list (noise stream)
+  AwType wt, gt, ct;
+  unsigned char vec;               // every pointer aligned for the wide path
+};
+
+struct AwTable {
+  int n;
+  unsigned chunks;                 // first[n]
+  unsigned first[AW_MAX + 1];      // first chunk of each tensor
+  AwTensor t[AW_MAX];
+};
+
+struct AwHyper {
+  float b1, c1, b2, c2;            // beta, 1 - beta
+  float eps;
+  float lr, rate, root;            // lr, lr / (1 - b1^t), 1 / sqrt(1 - b2^t) of a step given by the host
+  float log_b1, log_b2;            // for a step read on the device
+  int bias, stochastic;
+  unsigned long long seed;
+  long long step;
+  const float* lr_dev;
+  const long long* step_dev;
+  const float* gscale;
+  const int* skip;
+};
+
+struct ClipArgs {
+  double* partial;                 // one sum of squares per CTA
+  int parts;                       // number of partial sums
+  float max_norm;
+  const float* scale;              // optional factor of the gradients
+  float* norm;
+  float* factor;
+  int* nonfinite;                  // optional
+};
+
+constexpr int CLIP_MAX_CTAS = 8192;   // partial sums of one call
+
+cudaError_t launch_adamw(const AwTable& t, const AwHyper& h, cudaStream_t s);
+cudaError_t launch_adamw8(const AwTable& t, const AwHyper& h, cudaStream_t s);
+cudaError_t launch_pack(const AwTable& t, const AwHyper& h, cudaStream_t s);
+cudaError_t launch_unpack(const AwTable& t, cudaStream_t s);
+// CTAs of the norm launch over `chunks` chunks (its number of partial sums), at most `most`
+int clip_norm_ctas(unsigned chunks, int most);
+cudaError_t launch_clip_norm(const AwTable& t, double* partial, int ctas, cudaStream_t s);
+cudaError_t launch_clip_finish(const ClipArgs& a, cudaStream_t s);
+cudaError_t launch_clip_scale(const AwTable& t, const float* factor, cudaStream_t s);
+
+}  // namespace mo

@@ -540,5 +540,10 @@ mo_status mo_gemm_bf16(mo_ctx* ctx, const mo_gemm_desc* d, void* stream) {
 // Accessors for entry points defined in other translation units.
 namespace mo {
 int ctx_device(const mo_ctx* ctx) { return ctx->device; }
+char* ctx_workspace(const mo_ctx* ctx, size_t* bytes) {
+  *bytes = ctx->ws_bytes;
+  return ctx->ws;
+}
+Profiler* ctx_profiler(mo_ctx* ctx) { return ctx->profiling ? &ctx->prof : nullptr; }
 mo_status ctx_fail(mo_ctx* ctx, mo_status st, const std::string& msg) { return fail(ctx, st, msg); }
 }  // namespace mo

@@ -27,7 +27,10 @@ enum ProfKind {
   PK_QR_TRAIL = 13,  // QR: tensor-core trailing updates
   PK_SMALL = 14,     // fused small-matrix Newton-Schulz / Muon
   PK_TABLES = 15,    // device pointer-table uploads
-  PK_COUNT = 16
+  PK_ADAMW = 16,     // AdamW step over many tensors
+  PK_MOMENTS = 17,   // 8-bit moments: pack, unpack
+  PK_CLIP = 18,      // gradient norm, clip factor, scaling
+  PK_COUNT = 19
 };
 
 struct ProfRec {

@@ -21,6 +21,9 @@ in our own code, and follows its steps in the order the pages give them:
               refresh ("LLM Optimizers ...", section 11.1 equations;
               "Reading notes on SOAP, Muon, and Beyond", sections 1 and 4;
               "初探优化器（一）", section 6.2).
+* ``adamw`` - AdamW for what is not a matrix ("LLM Optimizers ...", sections
+              5 and 6), its moments in 8 bits, and clipping by the global
+              norm (section 7.4).
 * ``qr``    - the QR factorisation with the positive-diagonal convention.
 * ``bf16``  - round-to-nearest-even rounding to bfloat16, used by the
               emulation modes that reproduce the GPU path's declared
@@ -31,4 +34,4 @@ Pins (what this oracle is checked against, independently of itself) live in
 least one pin; none is "parity unpinned".
 """
 
-from . import bf16, ns, muon, qr, soap  # noqa: F401
+from . import adamw, bf16, ns, muon, qr, soap  # noqa: F401
