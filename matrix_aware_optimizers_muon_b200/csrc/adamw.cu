@@ -17,6 +17,9 @@
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
+#include <type_traits>
+#include <utility>
+
 #include "profile.h"
 #include "ptx.cuh"
 #include "runtime.h"
@@ -25,119 +28,205 @@ namespace mo {
 
 namespace {
 
+#ifndef STEP8_CTAS
+#define STEP8_CTAS 24
+#endif
+#ifndef STEP32_CTAS
+#define STEP32_CTAS 24
+#endif
 constexpr int PER = AW_BLOCK / 32;     // elements of a lane
 
-// A warp's block of a tensor.
-struct Block {
-  size_t off;        // first element
-  int left;          // elements of the block inside the tensor (1..256)
-  bool wide;
-  int lane;
-  __device__ __forceinline__ int at(int j) const { return wide ? lane * PER + j : lane + 32 * j; }
-  __device__ __forceinline__ bool has(int j) const { return wide || lane + 32 * j < left; }
+// A lane's place in a block: wide lanes hold 8 neighbours, narrow ones elements
+// 32 apart.
+template <bool WIDE>
+struct Place {
+  unsigned long long first;   // the lane's first element
+  int left;                   // narrow: elements of the tensor from there on
+  __device__ __forceinline__ bool has(int j) const { return WIDE || 32 * j < left; }
 };
 
-__device__ __forceinline__ float widen(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ float widen(__half x) { return __half2float(x); }
-__device__ __forceinline__ float widen(float x) { return x; }
-template <typename T>
-__device__ __forceinline__ T narrow(float x);
-template <>
-__device__ __forceinline__ float narrow<float>(float x) { return x; }
-template <>
-__device__ __forceinline__ __nv_bfloat16 narrow<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
-template <>
-__device__ __forceinline__ __half narrow<__half>(float x) { return __float2half_rn(x); }
+// ---------------------------------------------------------------- loads and stores
+using Code = unsigned char;            // of an 8-bit moment
 
+// A lane's 8 elements of a tensor as they are stored, 16-bit ones two and codes
+// four to a word.
 template <typename T>
-struct alignas(sizeof(T) * PER) Pack {
-  T x[PER];
+struct Raw {
+  static constexpr int WORDS = PER * sizeof(T) / 4;
+  unsigned w[WORDS];
 };
 
-template <typename T>
-__device__ __forceinline__ void load_as(float (&x)[PER], const void* p, const Block& b) {
-  const T* q = static_cast<const T*>(p) + b.off;
-  if (b.wide) {
-    const Pack<T> v = *reinterpret_cast<const Pack<T>*>(q + b.lane * PER);
-#pragma unroll
-    for (int j = 0; j < PER; ++j) x[j] = widen(v.x[j]);
+__device__ __forceinline__ unsigned bits_of(float x) { return __float_as_uint(x); }
+__device__ __forceinline__ unsigned bits_of(__nv_bfloat16 x) { return __bfloat16_as_ushort(x); }
+__device__ __forceinline__ unsigned bits_of(unsigned char x) { return x; }
+__device__ __forceinline__ unsigned bits_of(__half x) { return __half_as_ushort(x); }
+
+// One access of 32 or 16 bytes (two of 16 for fp32 would each touch half of
+// every 32-byte sector), `AT` bytes behind p.
+template <int AT>
+__device__ __forceinline__ void load_words(unsigned (&w)[8], const void* p) {
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8 + %9];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+               : "l"(p), "n"(AT)
+               : "memory");
+}
+template <int AT>
+__device__ __forceinline__ void load_words(unsigned (&w)[4], const void* p) {
+  asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4 + %5];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+               : "l"(p), "n"(AT)
+               : "memory");
+}
+template <int AT>
+__device__ __forceinline__ void load_words(unsigned (&w)[2], const void* p) {
+  asm volatile("ld.global.v2.b32 {%0, %1}, [%2 + %3];" : "=r"(w[0]), "=r"(w[1]) : "l"(p), "n"(AT) : "memory");
+}
+__device__ __forceinline__ void store_words(const unsigned (&w)[8], void* p) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+__device__ __forceinline__ void store_words(const unsigned (&w)[4], void* p) {
+  asm volatile("st.global.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
+}
+__device__ __forceinline__ void store_words(const unsigned (&w)[2], void* p) {
+  asm volatile("st.global.v2.b32 [%0], {%1, %2};" ::"l"(p), "r"(w[0]), "r"(w[1]) : "memory");
+}
+
+// p is the lane's first element; a wide lane may read AT blocks further on.
+template <bool WIDE, int AT = 0, typename T>
+__device__ __forceinline__ void fetch(Raw<T>& r, const T* p, const Place<WIDE>& b) {
+  if (WIDE) {
+    load_words<AT * AW_BLOCK * (int)sizeof(T)>(r.w, p);
   } else {
+    constexpr int IN = 4 / sizeof(T);                  // elements of a word
 #pragma unroll
-    for (int j = 0; j < PER; ++j) x[j] = b.has(j) ? widen(q[b.at(j)]) : 0.f;
+    for (int k = 0; k < Raw<T>::WORDS; ++k) {
+      r.w[k] = 0;
+#pragma unroll
+      for (int j = IN * k; j < IN * (k + 1); ++j)
+        if (b.has(j)) r.w[k] |= bits_of(p[32 * j]) << (8 * sizeof(T) * (j % IN));
+    }
   }
 }
 
-template <typename T>
-__device__ __forceinline__ void store_as(const float (&x)[PER], void* p, const Block& b) {
-  T* q = static_cast<T*>(p) + b.off;
-  if (b.wide) {
-    Pack<T> v;
-#pragma unroll
-    for (int j = 0; j < PER; ++j) v.x[j] = narrow<T>(x[j]);
-    *reinterpret_cast<Pack<T>*>(q + b.lane * PER) = v;
+template <bool WIDE, typename T>
+__device__ __forceinline__ void put(const Raw<T>& r, T* p, const Place<WIDE>& b) {
+  if (WIDE) {
+    store_words(r.w, p);
   } else {
+    constexpr int IN = 4 / sizeof(T);
 #pragma unroll
-    for (int j = 0; j < PER; ++j)
-      if (b.has(j)) q[b.at(j)] = narrow<T>(x[j]);
+    for (int j = 0; j < PER; ++j) {
+      if (!b.has(j)) continue;
+      const unsigned x = r.w[j / IN] >> (8 * sizeof(T) * (j % IN));
+      if (IN == 1) reinterpret_cast<unsigned*>(p)[32 * j] = x;
+      else if (IN == 2) reinterpret_cast<unsigned short*>(p)[32 * j] = (unsigned short)x;
+      else reinterpret_cast<unsigned char*>(p)[32 * j] = (unsigned char)x;
+    }
   }
 }
 
-__device__ __forceinline__ void load(float (&x)[PER], const void* p, AwType t, const Block& b) {
-  if (t == AW_F32) load_as<float>(x, p, b);
-  else if (t == AW_BF16) load_as<__nv_bfloat16>(x, p, b);
-  else load_as<__half>(x, p, b);
-}
-
-__device__ __forceinline__ void store(const float (&x)[PER], void* p, AwType t, const Block& b) {
-  if (t == AW_F32) store_as<float>(x, p, b);
-  else if (t == AW_BF16) store_as<__nv_bfloat16>(x, p, b);
-  else store_as<__half>(x, p, b);
-}
-
-__device__ __forceinline__ void load_codes(unsigned char (&c)[PER], const void* p, const Block& b) {
-  const unsigned char* q = static_cast<const unsigned char*>(p) + b.off;
-  if (b.wide) {
-    const Pack<unsigned char> v = *reinterpret_cast<const Pack<unsigned char>*>(q + b.lane * PER);
+__device__ __forceinline__ void widen_all(float (&x)[PER], const Raw<float>& r) {
 #pragma unroll
-    for (int j = 0; j < PER; ++j) c[j] = v.x[j];
-  } else {
+  for (int j = 0; j < PER; ++j) x[j] = __uint_as_float(r.w[j]);
+}
+__device__ __forceinline__ void widen_all(float (&x)[PER], const Raw<__nv_bfloat16>& r) {
 #pragma unroll
-    for (int j = 0; j < PER; ++j) c[j] = b.has(j) ? q[b.at(j)] : 0;
+  for (int q = 0; q < PER / 2; ++q) {
+    x[2 * q] = __uint_as_float(r.w[q] << 16);
+    x[2 * q + 1] = __uint_as_float(r.w[q] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void widen_all(float (&x)[PER], const Raw<__half>& r) {
+#pragma unroll
+  for (int q = 0; q < PER / 2; ++q) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&r.w[q]));
+    x[2 * q] = f.x;
+    x[2 * q + 1] = f.y;
   }
 }
 
-__device__ __forceinline__ void store_codes(const unsigned char (&c)[PER], void* p, const Block& b) {
-  unsigned char* q = static_cast<unsigned char*>(p) + b.off;
-  if (b.wide) {
-    Pack<unsigned char> v;
+__device__ __forceinline__ void narrow_all(Raw<float>& r, const float (&x)[PER]) {
 #pragma unroll
-    for (int j = 0; j < PER; ++j) v.x[j] = c[j];
-    *reinterpret_cast<Pack<unsigned char>*>(q + b.lane * PER) = v;
-  } else {
+  for (int j = 0; j < PER; ++j) r.w[j] = __float_as_uint(x[j]);
+}
+__device__ __forceinline__ void narrow_all(Raw<__nv_bfloat16>& r, const float (&x)[PER]) {
 #pragma unroll
-    for (int j = 0; j < PER; ++j)
-      if (b.has(j)) q[b.at(j)] = c[j];
+  for (int q = 0; q < PER / 2; ++q) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * q], x[2 * q + 1]);
+    r.w[q] = *reinterpret_cast<const unsigned*>(&h);
+  }
+}
+__device__ __forceinline__ void narrow_all(Raw<__half>& r, const float (&x)[PER]) {
+#pragma unroll
+  for (int q = 0; q < PER / 2; ++q) {
+    const __half2 h = __floats2half2_rn(x[2 * q], x[2 * q + 1]);
+    r.w[q] = *reinterpret_cast<const unsigned*>(&h);
   }
 }
 
-// Tensor of chunk c (the last one whose first chunk is at most c).
-__device__ __forceinline__ int find(const AwTable& tab, unsigned c) {
-  int lo = 0, hi = tab.n - 1;
+template <bool WIDE, typename T>
+__device__ __forceinline__ void store(const float (&x)[PER], T* p, const Place<WIDE>& b) {
+  Raw<T> r;
+  narrow_all(r, x);
+  put(r, p, b);
+}
+
+// ---------------------------------------------------------------- the list
+// Tensor that holds run `run` of the list, none before tensor i.
+__device__ __forceinline__ int find(const AwTable& tab, unsigned run, int i) {
+  if (run < tab.first[i + 1]) return i;
+  int lo = i + 1, hi = tab.n - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (tab.first[mid] <= c) lo = mid; else hi = mid - 1;
+    if (tab.first[mid] <= run) lo = mid; else hi = mid - 1;
   }
   return lo;
 }
 
-__device__ __forceinline__ bool block_of(Block& b, const AwTensor& t, unsigned chunk) {
-  b.off = (size_t)chunk * AW_CHUNK + (threadIdx.x >> 5) * AW_BLOCK;
-  if ((long long)b.off >= t.numel) return false;
-  const long long left = t.numel - (long long)b.off;
-  b.left = left < AW_BLOCK ? (int)left : AW_BLOCK;
-  b.wide = t.vec && b.left == AW_BLOCK;
-  b.lane = threadIdx.x & 31;
-  return true;
+// A CTA is one warp.  It takes every gridDim-th run of tab.run blocks of a
+// tensor and fetches a block while it works on the one before.
+//   Op::start(tensor, first element, blocks)   a run begins
+//   Op::fetch<AT>(Load&, at)                   reads a whole block, AT blocks behind the lane's offset `at`
+//   Op::work(Load, Place, at, r)               works on block r of the run
+//   Op::narrow(tensor, Place, at, r)           reads and works on block r of a misaligned tensor (VEC false) or a partial one
+//   Op::finish(blocks)                         the run ends
+template <bool VEC, typename Op>
+__device__ __forceinline__ void walk(const AwTable& tab, Op& op) {
+  const unsigned lane = threadIdx.x;
+  int i = 0;
+  for (unsigned run = blockIdx.x; run < tab.runs; run += gridDim.x) {
+    i = find(tab, run, i);
+    const AwTensor& t = tab.t[i];
+    const long long block = (long long)(run - tab.first[i]) * tab.run;
+    const unsigned long long first = (unsigned long long)block * AW_BLOCK;
+    const int blocks = (int)min((long long)tab.run, (t.numel + AW_BLOCK - 1) / AW_BLOCK - block);
+    const int whole = VEC ? (int)min((long long)blocks, t.numel / AW_BLOCK - block) : 0;
+    op.start(t, first, blocks);
+    int r = 0;
+    if (whole > 0) {
+      unsigned at = lane * PER;
+      typename Op::Load even, odd;             // two buffers and two copies of the body: no moves between them
+      op.template fetch<0>(even, at);
+      while (true) {
+        if (r + 1 < whole) op.template fetch<1>(odd, at);
+        op.work(even, Place<true>{first + at, 0}, at, r);
+        at += AW_BLOCK;
+        if (++r == whole) break;
+        if (r + 1 < whole) op.template fetch<1>(even, at);
+        op.work(odd, Place<true>{first + at, 0}, at, r);
+        at += AW_BLOCK;
+        if (++r == whole) break;
+      }
+    }
+    for (; r < blocks; ++r) {
+      const unsigned at = (unsigned)r * AW_BLOCK + lane;
+      const long long left = t.numel - (long long)(first + at);
+      op.narrow(t, Place<false>{first + at, left < AW_BLOCK ? (int)left : AW_BLOCK}, at, r);
+    }
+    op.finish(blocks);
+  }
 }
 
 // ---------------------------------------------------------------- noise
@@ -150,8 +239,10 @@ struct Keys {
   unsigned k1, k2;
 };
 
-__device__ __forceinline__ Keys keys_of(unsigned long long seed, long long step, unsigned index) {
-  unsigned long long z = seed + (unsigned long long)step * 0x9E3779B97F4A7C15ull + index * 0xBB67AE8584CAA73Bull;
+__device__ __forceinline__ Keys keys_of(const AwHyper& h, unsigned index) {
+  if (!h.stochastic) return {0, 0};
+  const unsigned long long step = (unsigned long long)(h.step_dev ? *h.step_dev : h.step);
+  unsigned long long z = h.seed + step * 0x9E3779B97F4A7C15ull + index * 0xBB67AE8584CAA73Bull;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     z ^= z >> 32;
@@ -165,7 +256,7 @@ __device__ __forceinline__ unsigned first_word(unsigned long long pair, Keys k) 
   unsigned x = (unsigned)pair ^ k.k1;
   x *= 0x9E3779B9u;
   x ^= x >> 16;
-  x = x * 0x6A09E667u + k.k2 + (unsigned)(pair >> 32);
+  x = x * 0x6A09E667u + (k.k2 + (unsigned)(pair >> 32));
   x ^= x >> 15;
   x *= 0x9E3779B9u;
   return x ^ (x >> 16);
@@ -175,6 +266,34 @@ __device__ __forceinline__ unsigned second_word(unsigned first, Keys k) {
   const unsigned y = (first ^ k.k1) * 0x6A09E667u + k.k2;
   return y ^ (y >> 16);
 }
+
+// The first words that a lane's elements need: wide lanes hold whole pairs,
+// narrow ones an element of each.
+template <bool WIDE>
+struct Noise {
+  unsigned w[WIDE ? PER / 2 : PER];
+  __device__ __forceinline__ void draw(const Place<WIDE>& b, Keys k) {
+    const unsigned long long base = b.first >> 1;
+#pragma unroll
+    for (int q = 0; q < (WIDE ? PER / 2 : PER); ++q) w[q] = first_word(base + (WIDE ? q : 16 * q), k);
+  }
+  __device__ __forceinline__ Noise second(Keys k) const {
+    Noise n;
+#pragma unroll
+    for (int q = 0; q < (WIDE ? PER / 2 : PER); ++q) n.w[q] = second_word(w[q], k);
+    return n;
+  }
+  // Element j's 16 bits; and those with a half behind them in bits 7 to 23.
+  // (With byte permutations here nvcc 12.9 merged them with pack_tops's into
+  // wrong codes.)
+  __device__ __forceinline__ unsigned bits16(int j) const {
+    return (WIDE ? j : threadIdx.x) % 2 ? w[WIDE ? j / 2 : j] >> 16 : w[WIDE ? j / 2 : j] & 0xffffu;
+  }
+  __device__ __forceinline__ unsigned bits24(int j) const {
+    const unsigned x = w[WIDE ? j / 2 : j];
+    return (((WIDE ? j : threadIdx.x) % 2 ? x >> 8 : x << 8) & 0xffff00u) | 0x80u;
+  }
+};
 
 // ---------------------------------------------------------------- 8-bit moments
 // A block of 256 elements shares one scale 2^(s - 127) for each moment, a
@@ -187,79 +306,145 @@ __device__ __forceinline__ unsigned second_word(unsigned first, Keys k) {
 //      below half a step for the usual b2, and the nearest code would stay
 //      where it is.  v > 0 never gets code 0, which would leave eps alone in
 //      the denominator; code 255 stands for a value that is not finite.
-__device__ __forceinline__ unsigned magnitude(float x) {
-  const unsigned u = __float_as_uint(x) & 0x7fffffffu;
-  return u < 0x7f800000u ? u : 0u;
-}
+// An fp32 value times 2^(127 - s) 2^-112 has v's code in bits 20 to 27, its
+// subnormals included, and what is rounded off below them.
+constexpr unsigned INF_BITS = 0x7f800000u;
+constexpr unsigned HIGH_BITS = 0x4e000000u;   // 2^29: below, v's scale is at most 2^14
 
 // 2^(s - 127) of a scale byte; 2^-127 is subnormal
 __device__ __forceinline__ float scale_of(unsigned s) { return __uint_as_float(s ? s << 23 : 0x00400000u); }
-
-__device__ __forceinline__ float first_moment(unsigned char c, float scale) {
-  const __half_raw h = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)c, __NV_E4M3);
-  return __half2float(__half(h)) * scale;
+// Whether one of four codes of v is 248 or above.
+__device__ __forceinline__ bool has_high(unsigned w) {
+  const unsigned t = ~w & 0xf8f8f8f8u;
+  return ((t - 0x01010101u) & ~t & 0x80808080u) != 0;
 }
 
-__device__ __forceinline__ float second_moment(unsigned char c, float scale) {
-  const float v = __uint_as_float((unsigned)c << 20) * 0x1p112f * scale;
-  return c == 255 ? __uint_as_float(0x7fffffffu) : v;
-}
-
-// The block's scale bytes, from the warp's largest magnitudes.
-__device__ __forceinline__ unsigned scale_byte(const float (&x)[PER], int drop) {
-  unsigned big = 0;
+// Moments of a lane's codes, to be scaled.
+__device__ __forceinline__ void decode(float (&m)[PER], float (&v)[PER], const Raw<Code>& mc, const Raw<Code>& vc) {
 #pragma unroll
-  for (int j = 0; j < PER; ++j) big = max(big, magnitude(x[j]));
-  big = __reduce_max_sync(0xffffffffu, big);
-  return (unsigned)max(1, (int)(big >> 23) - drop);
+  for (int q = 0; q < PER / 2; ++q) {
+    const unsigned pair = q % 2 ? mc.w[q / 2] >> 16 : mc.w[q / 2] & 0xffffu;
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)pair, __NV_E4M3);
+    const float2 f = __half22float2(__half2(h));
+    m[2 * q] = f.x;
+    m[2 * q + 1] = f.y;
+  }
+  // v's codes below 248 are the upper bits of an fp16 number without its sign
+#pragma unroll
+  for (int q = 0; q < PER / 2; ++q) {
+    const unsigned w = vc.w[q / 2];
+    const unsigned h = (q % 2 ? __byte_perm(w, 0, 0x4342) : __byte_perm(w, 0, 0x4140)) << 7;
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    v[2 * q] = f.x;
+    v[2 * q + 1] = f.y;
+  }
+  if (has_high(vc.w[0]) || has_high(vc.w[1])) {
+    // 248 is 2^16, which a block's largest value may round up to; 255 is a NaN
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      const unsigned c = (vc.w[j / 4] >> (8 * (j % 4))) & 0xffu;
+      v[j] = c == 255u ? __uint_as_float(0x7fffffffu) : __uint_as_float(c << 20) * 0x1p112f;
+    }
+  }
 }
 
-__device__ __forceinline__ unsigned char first_code(float m, float inv) {
-  const float y = m * inv;
-  // an infinity has no e4m3 code: y + 0 y makes it a NaN and leaves the rest
-  return (unsigned char)__nv_cvt_float_to_fp8(fmaf(y, 0.f, y), __NV_SATFINITE, __NV_E4M3);
+// The scale bytes of a run, m's below v's, block r's in lane r: they are read
+// and written once for a run.  A byte at a time, reads of a 32-byte sector that
+// waits for other bytes made the step 1.5 times as long (218 M bf16 elements:
+// 975 us, and 615 without the stores).
+struct Scales {
+  unsigned all;
+  __device__ __forceinline__ void load(const Code* ms, const Code* vs, int blocks) {
+    all = 0;
+    if ((int)threadIdx.x < blocks) all = ms[threadIdx.x] | (unsigned)vs[threadIdx.x] << 8;
+  }
+  __device__ __forceinline__ unsigned of(int r) const { return __shfl_sync(0xffffffffu, all, r); }
+  __device__ __forceinline__ void set(int r, unsigned ms, unsigned vs) {
+    if ((int)threadIdx.x == r) all = ms | vs << 8;
+  }
+  __device__ __forceinline__ void store(Code* ms, Code* vs, int blocks) const {
+    if ((int)threadIdx.x < blocks) {
+      ms[threadIdx.x] = (Code)all;
+      vs[threadIdx.x] = (Code)(all >> 8);
+    }
+  }
+};
+
+__device__ __forceinline__ unsigned pack_tops(unsigned a, unsigned b, unsigned c, unsigned d) {
+  return __byte_perm(__byte_perm(a, b, 0x0073), __byte_perm(c, d, 0x0073), 0x5410);
 }
 
-__device__ __forceinline__ unsigned char second_code(float v, float inv, int stochastic, unsigned bits) {
-  const unsigned u = __float_as_uint(v * inv * 0x1p-112f);
-  const unsigned r = u + (stochastic ? bits * 16u + 8u : 0x7ffffu + ((u >> 20) & 1u));
-  const unsigned c = v > 0.f ? max(1u, r >> 20) : 0u;
-  return (unsigned char)(fabsf(v) < __uint_as_float(0x7f800000u) ? c : 255u);
-}
-
-__device__ __forceinline__ void load_moments(float (&m)[PER], float (&v)[PER], const AwTensor& t, const Block& b) {
-  unsigned char mc[PER], vc[PER];
-  load_codes(mc, t.M, b);
-  load_codes(vc, t.V, b);
-  const size_t k = b.off / AW_BLOCK;
-  const float ms = scale_of(t.MS[k]), vs = scale_of(t.VS[k]);
+// Codes of v in bits 24 to 31 of r; scaled is v times 2^(127 - s) 2^-112.
+template <bool STOCHASTIC, bool WIDE>
+__device__ __forceinline__ void second_codes(unsigned (&r)[PER], const float (&v)[PER], const float (&scaled)[PER],
+                                             const Noise<WIDE>& n) {
+  unsigned least = 0xffffffffu;
 #pragma unroll
   for (int j = 0; j < PER; ++j) {
-    m[j] = first_moment(mc[j], ms);
-    v[j] = second_moment(vc[j], vs);
+    const unsigned u = __float_as_uint(scaled[j]);
+    r[j] = STOCHASTIC ? u * 16u + n.bits24(j) : (u + 0x7ffffu + ((u >> 20) & 1u)) * 16u;
+    least = min(least, r[j]);
+  }
+  if (least < (1u << 24)) {
+#pragma unroll
+    for (int j = 0; j < PER; ++j)
+      if (v[j] > 0.f && r[j] < (1u << 24)) r[j] = 1u << 24;
   }
 }
 
-__device__ __forceinline__ void store_moments(const float (&m)[PER], const float (&v)[PER], const AwTensor& t,
-                                              const Block& b, int stochastic, Keys k) {
-  const unsigned ms = scale_byte(m, 7), vs = scale_byte(v, 15);
-  const float mi = __uint_as_float((254u - ms) << 23), vi = __uint_as_float((254u - vs) << 23);
-  unsigned char mc[PER], vc[PER];
+template <bool WIDE>
+__device__ __forceinline__ void store_moments(float (&m)[PER], float (&v)[PER], Code* mp, Code* vp, Scales& scales, int r,
+                                              const Place<WIDE>& b, bool stochastic, const Noise<WIDE>& n) {
+  float bm = 0.f;
+  unsigned bv = 0;
 #pragma unroll
   for (int j = 0; j < PER; ++j) {
-    const unsigned long long e = b.off + b.at(j);
-    unsigned bits = 0;
-    if (stochastic) bits = (first_word(e >> 1, k) >> (16 * (e & 1))) & 0xffffu;
-    mc[j] = first_code(m[j], mi);
-    vc[j] = second_code(v[j], vi, stochastic, bits);
+    bm = fmaxf(bm, fabsf(m[j]));                       // leaves NaN out
+    bv = max(bv, __float_as_uint(v[j]));               // infinite, NaN and negative values come out largest
   }
-  store_codes(mc, t.M, b);
-  store_codes(vc, t.V, b);
-  if (b.lane == 0) {
-    const size_t at = b.off / AW_BLOCK;
-    t.MS[at] = (unsigned char)ms;
-    t.VS[at] = (unsigned char)vs;
+  unsigned um = __reduce_max_sync(0xffffffffu, __float_as_uint(bm));
+  unsigned uv = __reduce_max_sync(0xffffffffu, bv);
+  unsigned odd = 0;                                    // elements whose v has code 255
+  float scaled[PER];
+  unsigned ms, vs;
+  if (um < INF_BITS && uv < HIGH_BITS) {
+    ms = max(1, (int)(um >> 23) - 7);
+    vs = max(1, (int)(uv >> 23) - 15);
+    const float vi = __uint_as_float((142u - vs) << 23);   // 2^(127 - s) 2^-112, a normal number below HIGH_BITS
+#pragma unroll
+    for (int j = 0; j < PER; ++j) scaled[j] = v[j] * vi;
+  } else {
+    // the scale is that of the finite values; an infinite m has no code and becomes a NaN
+    um = uv = 0;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      const unsigned a = __float_as_uint(fabsf(m[j])), c = __float_as_uint(fabsf(v[j]));
+      if (a < INF_BITS) um = max(um, a); else m[j] = __uint_as_float(0x7fffffffu);
+      if (c < INF_BITS) uv = max(uv, c); else odd |= 1u << j;
+      if (c >= INF_BITS || v[j] < 0.f) v[j] = 0.f;
+    }
+    um = __reduce_max_sync(0xffffffffu, um);
+    uv = __reduce_max_sync(0xffffffffu, uv);
+    ms = max(1, (int)(um >> 23) - 7);
+    vs = max(1, (int)(uv >> 23) - 15);
+#pragma unroll
+    for (int j = 0; j < PER; ++j) scaled[j] = v[j] * __uint_as_float((254u - vs) << 23) * 0x1p-112f;
   }
+  const float mi = __uint_as_float((254u - ms) << 23);
+  unsigned mw[PER / 2], vr[PER];
+#pragma unroll
+  for (int q = 0; q < PER / 2; ++q)
+    mw[q] = __nv_cvt_float2_to_fp8x2(make_float2(m[2 * q] * mi, m[2 * q + 1] * mi), __NV_SATFINITE, __NV_E4M3);
+  if (stochastic) second_codes<true>(vr, v, scaled, n);
+  else second_codes<false>(vr, v, scaled, n);
+  if (odd != 0) {
+#pragma unroll
+    for (int j = 0; j < PER; ++j)
+      if (odd & (1u << j)) vr[j] = 255u << 24;
+  }
+  put(Raw<Code>{{__byte_perm(mw[0], mw[1], 0x5410), __byte_perm(mw[2], mw[3], 0x5410)}}, mp, b);
+  put(Raw<Code>{{pack_tops(vr[0], vr[1], vr[2], vr[3]), pack_tops(vr[4], vr[5], vr[6], vr[7])}}, vp, b);
+  scales.set(r, ms, vs);
 }
 
 // ---------------------------------------------------------------- the step
@@ -283,103 +468,336 @@ __device__ __forceinline__ Rates rates_of(const AwHyper& h, const AwTensor& t) {
   return {rate * t.lr_scale, fmaf(-lr * t.lr_scale, t.wd, 1.f), root};
 }
 
+// sqrt and reciprocal of the hardware's special-function unit (2^-22 and
+// 2^-23 relative): the update they scale is a small part of the weight.  The
+// forms that take subnormal numbers as zeros need two instructions, the others
+// ten; they change a denominator by less than 2^-63 / sqrt(1 - b2), which is
+// nothing beside any eps of 1e-10 or more.
+template <bool TINY>
+__device__ __forceinline__ float sqrt_fast(float x) {
+  float r;
+  if (TINY) asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  else asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+template <bool TINY>
+__device__ __forceinline__ float reciprocal_fast(float x) {
+  float r;
+  if (TINY) asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  else asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+template <bool TINY>
+__device__ __forceinline__ float new_weight(float w, float m, float v, const Rates& r, float eps) {
+  const float den = fmaf(sqrt_fast<TINY>(v), r.root, eps);
+  return fmaf(r.decay, w, -(r.rate * m) * reciprocal_fast<TINY>(den));
+}
+
+// m and v come in units of the scales ms and vs, powers of two that the
+// constants take up exactly (fp32 moments: 1).
 __device__ __forceinline__ void update(float (&w)[PER], float (&m)[PER], float (&v)[PER], const float (&g)[PER],
-                                       const AwHyper& h, const Rates& r) {
+                                       const AwHyper& h, const Rates& r, float ms, float vs) {
+  const float b1 = h.b1 * ms, b2 = h.b2 * vs;
 #pragma unroll
   for (int j = 0; j < PER; ++j) {
-    m[j] = __fadd_rn(__fmul_rn(h.b1, m[j]), __fmul_rn(h.c1, g[j]));
-    v[j] = __fadd_rn(__fmul_rn(h.b2, v[j]), __fmul_rn(h.c2, __fmul_rn(g[j], g[j])));
-    const float den = fmaf(sqrtf(v[j]), r.root, h.eps);
-    w[j] = fmaf(r.decay, w[j], -(r.rate * m[j]) / den);
+    m[j] = __fadd_rn(__fmul_rn(b1, m[j]), __fmul_rn(h.c1, g[j]));
+    v[j] = __fadd_rn(__fmul_rn(b2, v[j]), __fmul_rn(h.c2, __fmul_rn(g[j], g[j])));
+  }
+  if (h.eps >= 1e-10f) {
+#pragma unroll
+    for (int j = 0; j < PER; ++j) w[j] = new_weight<false>(w[j], m[j], v[j], r, h.eps);
+  } else {
+#pragma unroll
+    for (int j = 0; j < PER; ++j) w[j] = new_weight<true>(w[j], m[j], v[j], r, h.eps);
   }
 }
 
 // bf16 weights without an fp32 master: to the neighbour above with the
 // probability of the distance, so that updates below half a step are not lost
-__device__ __forceinline__ void round_weights(float (&w)[PER], const Block& b, Keys k) {
+template <bool WIDE>
+__device__ __forceinline__ void round_weights(Raw<__nv_bfloat16>& out, const float (&w)[PER], const Noise<WIDE>& n) {
+  float zero = 0.f;                                    // NaN when a weight is not finite
 #pragma unroll
-  for (int j = 0; j < PER; ++j) {
-    const unsigned long long e = b.off + b.at(j);
-    const unsigned bits = (second_word(first_word(e >> 1, k), k) >> (16 * (e & 1))) & 0xffffu;
-    const unsigned u = __float_as_uint(w[j]);
-    if ((u & 0x7fffffffu) < 0x7f800000u) w[j] = __uint_as_float((u + bits) & 0xffff0000u);
+  for (int j = 0; j < PER; ++j) zero = fmaf(w[j], 0.f, zero);
+  unsigned u[PER];
+#pragma unroll
+  for (int j = 0; j < PER; ++j) u[j] = __float_as_uint(w[j]) + n.bits16(j);
+  if (zero != 0.f) {                                   // the sum may have made a number of a NaN
+#pragma unroll
+    for (int j = 0; j < PER; ++j)
+      if (!(fabsf(w[j]) < __uint_as_float(INF_BITS))) u[j] = __float_as_uint(w[j]);
+  }
+#pragma unroll
+  for (int q = 0; q < PER / 2; ++q) out.w[q] = __byte_perm(u[2 * q], u[2 * q + 1], 0x7632);
+}
+
+template <bool EIGHT, typename WT, typename GT>
+struct StepLoad {
+  using Moment = typename std::conditional<EIGHT, Code, float>::type;
+  Raw<WT> w;
+  Raw<GT> g;
+  Raw<Moment> m, v;
+};
+
+// What a tensor's elements share in a step.
+struct Shared {
+  Rates r;
+  Keys k;
+  AwType ct;
+  __device__ __forceinline__ void start(const AwHyper& h, const AwTensor& t) {
+    r = rates_of(h, t);
+    k = keys_of(h, t.index);
+    ct = t.ct;
+  }
+};
+
+__device__ __forceinline__ void moments_of(float (&m)[PER], float (&v)[PER], const Raw<float>& mr, const Raw<float>& vr, float&,
+                                           float&, unsigned) {
+  widen_all(m, mr);
+  widen_all(v, vr);
+}
+__device__ __forceinline__ void moments_of(float (&m)[PER], float (&v)[PER], const Raw<Code>& mc, const Raw<Code>& vc, float& ms,
+                                           float& vs, unsigned scales) {
+  decode(m, v, mc, vc);
+  const unsigned msb = scales & 0xffu, vsb = scales >> 8;
+  ms = scale_of(msb);
+  vs = scale_of(vsb);
+  if (min(msb, vsb) < 32) {
+    // b1 ms or b2 vs may be subnormal and not exact: scale the moments themselves
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      m[j] *= ms;
+      v[j] *= vs;
+    }
+    ms = vs = 1.f;
   }
 }
 
-template <bool EIGHT>
-__global__ void __launch_bounds__(AW_THREADS) adamw_kernel(const __grid_constant__ AwTable tab,
-                                                           const __grid_constant__ AwHyper h) {
+template <bool EIGHT, typename WT, typename GT, bool VEC>
+struct StepOp {
+  using Load = StepLoad<EIGHT, WT, GT>;
+  using Moment = typename Load::Moment;
+  const AwHyper& h;
+  float gs;
+  // the run's buffers: pointers that are the same in all threads; lanes add their 32-bit offset
+  WT* w;
+  const GT* g;
+  Moment* m;
+  Moment* v;
+  Code* ms;
+  Code* vs;
+  unsigned short* c;           // the copy's 16-bit elements
+  Shared s;
+  Scales scales;
+
+  __device__ __forceinline__ StepOp(const AwHyper& hyper, float scale) : h(hyper), gs(scale) {}
+  __device__ __forceinline__ void point(const AwTensor& t, unsigned long long first) {
+    w = static_cast<WT*>(t.W) + first;
+    g = static_cast<const GT*>(t.G) + first;
+    m = static_cast<Moment*>(t.M) + first;
+    v = static_cast<Moment*>(t.V) + first;
+    c = static_cast<unsigned short*>(t.C) + first;
+    s.start(h, t);
+  }
+  __device__ __forceinline__ void start(const AwTensor& t, unsigned long long first, int blocks) {
+    point(t, first);
+    if (EIGHT) {
+      ms = t.MS + first / AW_BLOCK;
+      vs = t.VS + first / AW_BLOCK;
+      scales.load(ms, vs, blocks);
+    }
+  }
+  template <int AT, bool WIDE = true>
+  __device__ __forceinline__ void fetch(Load& in, unsigned at, const Place<WIDE>& b = {}) const {
+    mo::fetch<WIDE, AT>(in.g, g + at, b);
+    mo::fetch<WIDE, AT>(in.w, w + at, b);
+    mo::fetch<WIDE, AT>(in.m, m + at, b);
+    mo::fetch<WIDE, AT>(in.v, v + at, b);
+  }
+  template <bool WIDE>
+  __device__ __forceinline__ void work(const Load& in, const Place<WIDE>& b, unsigned at, int r) {
+    float w1[PER], g1[PER], m1[PER], v1[PER];
+    widen_all(g1, in.g);
+    widen_all(w1, in.w);
+    if (h.gscale != nullptr) {
+#pragma unroll
+      for (int j = 0; j < PER; ++j) g1[j] *= gs;
+    }
+    float sm = 1.f, sv = 1.f;
+    moments_of(m1, v1, in.m, in.v, sm, sv, EIGHT ? scales.of(r) : 0);
+    update(w1, m1, v1, g1, h, s.r, sm, sv);
+    constexpr bool LOW = sizeof(WT) == 2;
+    Noise<WIDE> n;
+    if ((EIGHT || LOW) && h.stochastic) n.draw(b, s.k);
+    if constexpr (EIGHT) {
+      store_moments(m1, v1, m + at, v + at, scales, r, b, h.stochastic != 0, n);
+    } else {
+      store(m1, m + at, b);
+      store(v1, v + at, b);
+    }
+    if (!LOW && s.ct == AW_BF16) store(w1, reinterpret_cast<__nv_bfloat16*>(c) + at, b);
+    if (!LOW && s.ct == AW_F16) store(w1, reinterpret_cast<__half*>(c) + at, b);
+    if constexpr (LOW) {
+      Raw<WT> out;
+      if (h.stochastic) round_weights(out, w1, n.second(s.k));
+      else narrow_all(out, w1);
+      put(out, w + at, b);
+    } else {
+      store(w1, w + at, b);
+    }
+  }
+  __device__ __forceinline__ void work_narrow(const Place<false>& b, unsigned at, int r) {
+    Load in;
+    fetch<0, false>(in, at, b);
+    work(in, b, at, r);
+  }
+  __device__ __forceinline__ void narrow(const AwTensor& t, const Place<false>& b, unsigned at, int r);
+  __device__ __forceinline__ void finish(int blocks) const {
+    if (EIGHT) scales.store(ms, vs, blocks);
+  }
+};
+
+// The partial block of an aligned tensor, apart from the registers of the main
+// path; returns the run's scales.
+template <bool EIGHT, typename WT, typename GT>
+__device__ __noinline__ unsigned step_tail(const AwTensor& t, const AwHyper& h, float gs, unsigned long long first, int left,
+                                           unsigned scales, int r) {
+  StepOp<EIGHT, WT, GT, false> op(h, gs);
+  op.point(t, first - threadIdx.x);
+  op.scales.all = scales;
+  op.work_narrow(Place<false>{first, left}, threadIdx.x, r);
+  return op.scales.all;
+}
+
+template <bool EIGHT, typename WT, typename GT, bool VEC>
+__device__ __forceinline__ void StepOp<EIGHT, WT, GT, VEC>::narrow(const AwTensor& t, const Place<false>& b, unsigned at, int r) {
+  if (VEC) scales.all = step_tail<EIGHT, WT, GT>(t, h, gs, b.first, b.left, EIGHT ? scales.all : 0, r);
+  else work_narrow(b, at, r);
+}
+
+template <bool EIGHT, typename WT, typename GT, bool VEC>
+__global__ void __launch_bounds__(AW_THREADS, EIGHT ? STEP8_CTAS : STEP32_CTAS)
+    adamw_kernel(const __grid_constant__ AwTable tab, const __grid_constant__ AwHyper h) {
   pdl_wait();
   pdl_trigger();
   if (h.skip != nullptr && *h.skip != 0) return;
-  const float gs = h.gscale ? *h.gscale : 1.f;
-  for (unsigned c = blockIdx.x; c < tab.chunks; c += gridDim.x) {
-    const int i = find(tab, c);
-    const AwTensor& t = tab.t[i];
-    Block b;
-    if (!block_of(b, t, c - tab.first[i])) continue;
-    float w[PER], g[PER], m[PER], v[PER];
-    load(g, t.G, t.gt, b);
-    load(w, t.W, t.wt, b);
-    if (EIGHT) {
-      load_moments(m, v, t, b);
-    } else {
-      load_as<float>(m, t.M, b);
-      load_as<float>(v, t.V, b);
-    }
-    if (h.gscale != nullptr) {
-#pragma unroll
-      for (int j = 0; j < PER; ++j) g[j] *= gs;
-    }
-    update(w, m, v, g, h, rates_of(h, t));
-    Keys k = {0, 0};
-    if (h.stochastic) k = keys_of(h.seed, h.step_dev ? *h.step_dev : h.step, t.index);
-    if (EIGHT) {
-      store_moments(m, v, t, b, h.stochastic, k);
-    } else {
-      store_as<float>(m, t.M, b);
-      store_as<float>(v, t.V, b);
-    }
-    if (t.ct != AW_NONE) store(w, t.C, t.ct, b);
-    if (h.stochastic && t.wt == AW_BF16) round_weights(w, b, k);
-    store(w, t.W, t.wt, b);
-  }
+  StepOp<EIGHT, WT, GT, VEC> op(h, h.gscale ? *h.gscale : 1.f);
+  walk<VEC>(tab, op);
 }
 
+// ---------------------------------------------------------------- pack and unpack
+template <typename T>
+struct PackOp {
+  struct Load {
+    Raw<T> m, v;
+  };
+  const AwHyper& h;
+  const T* m;
+  const T* v;
+  Code* m8;
+  Code* v8;
+  Code* ms;
+  Code* vs;
+  Keys k;
+  Scales scales;
+  __device__ __forceinline__ explicit PackOp(const AwHyper& hyper) : h(hyper) {}
+  __device__ __forceinline__ void start(const AwTensor& t, unsigned long long first, int) {
+    m = static_cast<const T*>(t.G) + first;
+    v = static_cast<const T*>(t.C) + first;
+    m8 = static_cast<Code*>(t.M) + first;
+    v8 = static_cast<Code*>(t.V) + first;
+    ms = t.MS + first / AW_BLOCK;
+    vs = t.VS + first / AW_BLOCK;
+    k = keys_of(h, t.index);
+    scales.all = 0;
+  }
+  template <int AT, bool WIDE = true>
+  __device__ __forceinline__ void fetch(Load& in, unsigned at, const Place<WIDE>& b = {}) const {
+    mo::fetch<WIDE, AT>(in.m, m + at, b);
+    mo::fetch<WIDE, AT>(in.v, v + at, b);
+  }
+  template <bool WIDE>
+  __device__ __forceinline__ void work(const Load& in, const Place<WIDE>& b, unsigned at, int r) {
+    float x[PER], y[PER];
+    widen_all(x, in.m);
+    widen_all(y, in.v);
+    Noise<WIDE> n;
+    if (h.stochastic) n.draw(b, k);
+    store_moments(x, y, m8 + at, v8 + at, scales, r, b, h.stochastic != 0, n);
+  }
+  __device__ __forceinline__ void narrow(const AwTensor&, const Place<false>& b, unsigned at, int r) {
+    Load in;
+    fetch<0, false>(in, at, b);
+    work(in, b, at, r);
+  }
+  __device__ __forceinline__ void finish(int blocks) const { scales.store(ms, vs, blocks); }
+};
+
+template <typename T, bool VEC>
 __global__ void __launch_bounds__(AW_THREADS) pack_kernel(const __grid_constant__ AwTable tab,
                                                           const __grid_constant__ AwHyper h) {
   pdl_wait();
   pdl_trigger();
-  for (unsigned c = blockIdx.x; c < tab.chunks; c += gridDim.x) {
-    const int i = find(tab, c);
-    const AwTensor& t = tab.t[i];
-    Block b;
-    if (!block_of(b, t, c - tab.first[i])) continue;
-    float m[PER], v[PER];
-    load(m, t.G, t.gt, b);
-    load(v, t.C, t.gt, b);
-    Keys k = {0, 0};
-    if (h.stochastic) k = keys_of(h.seed, h.step_dev ? *h.step_dev : h.step, t.index);
-    store_moments(m, v, t, b, h.stochastic, k);
-  }
+  PackOp<T> op(h);
+  walk<VEC>(tab, op);
 }
 
+template <typename T>
+struct UnpackOp {
+  struct Load {
+    Raw<Code> m, v;
+  };
+  const Code* m8;
+  const Code* v8;
+  T* m;
+  T* v;
+  Scales scales;
+  __device__ __forceinline__ void start(const AwTensor& t, unsigned long long first, int blocks) {
+    m8 = static_cast<const Code*>(t.M) + first;
+    v8 = static_cast<const Code*>(t.V) + first;
+    m = static_cast<T*>(t.W) + first;
+    v = static_cast<T*>(t.C) + first;
+    scales.load(t.MS + first / AW_BLOCK, t.VS + first / AW_BLOCK, blocks);
+  }
+  template <int AT, bool WIDE = true>
+  __device__ __forceinline__ void fetch(Load& in, unsigned at, const Place<WIDE>& b = {}) const {
+    mo::fetch<WIDE, AT>(in.m, m8 + at, b);
+    mo::fetch<WIDE, AT>(in.v, v8 + at, b);
+  }
+  template <bool WIDE>
+  __device__ __forceinline__ void work(const Load& in, const Place<WIDE>& b, unsigned at, int r) const {
+    float x[PER], y[PER];
+    decode(x, y, in.m, in.v);
+    const unsigned sc = scales.of(r);
+    const float sm = scale_of(sc & 0xffu), sv = scale_of(sc >> 8);
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      x[j] *= sm;
+      y[j] *= sv;
+    }
+    store(x, m + at, b);
+    store(y, v + at, b);
+  }
+  __device__ __forceinline__ void narrow(const AwTensor&, const Place<false>& b, unsigned at, int r) const {
+    Load in;
+    fetch<0, false>(in, at, b);
+    work(in, b, at, r);
+  }
+  __device__ __forceinline__ void finish(int) const {}
+};
+
+template <typename T, bool VEC>
 __global__ void __launch_bounds__(AW_THREADS) unpack_kernel(const __grid_constant__ AwTable tab) {
   pdl_wait();
   pdl_trigger();
-  for (unsigned c = blockIdx.x; c < tab.chunks; c += gridDim.x) {
-    const int i = find(tab, c);
-    const AwTensor& t = tab.t[i];
-    Block b;
-    if (!block_of(b, t, c - tab.first[i])) continue;
-    float m[PER], v[PER];
-    load_moments(m, v, t, b);
-    store(m, t.W, t.wt, b);
-    store(v, t.C, t.wt, b);
-  }
+  UnpackOp<T> op;
+  walk<VEC>(tab, op);
 }
 
 // ---------------------------------------------------------------- clipping
+constexpr int FINISH_THREADS = 256;
+
 // norm    sum of squares: 8 at a time in fp32, then fp64; one partial sum per
 //         CTA, in an order that the grid alone fixes
 // finish  the partial sums in a fixed order, the norm and the factor
@@ -390,47 +808,53 @@ __device__ __forceinline__ double warp_sum(double x) {
   return x;
 }
 
-// Sum over the CTA, in thread 0.
-__device__ __forceinline__ double cta_sum(double x) {
-  __shared__ double red[AW_THREADS / 32];
-  x = warp_sum(x);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
-  __syncthreads();
-  double s = 0.0;
-  if (threadIdx.x == 0) {
+template <typename T>
+struct NormOp {
+  using Load = Raw<T>;
+  double sum = 0.0;
+  const T* g;
+  __device__ __forceinline__ void start(const AwTensor& t, unsigned long long first, int) { g = static_cast<const T*>(t.G) + first; }
+  template <int AT, bool WIDE = true>
+  __device__ __forceinline__ void fetch(Load& in, unsigned at, const Place<WIDE>& b = {}) const { mo::fetch<WIDE, AT>(in, g + at, b); }
+  template <bool WIDE>
+  __device__ __forceinline__ void work(const Load& in, const Place<WIDE>&, unsigned, int) {
+    float x[PER], s = 0.f;
+    widen_all(x, in);
 #pragma unroll
-    for (int k = 0; k < AW_THREADS / 32; ++k) s += red[k];
+    for (int j = 0; j < PER; ++j) s = fmaf(x[j], x[j], s);
+    sum += (double)s;
   }
-  return s;
-}
+  __device__ __forceinline__ void narrow(const AwTensor&, const Place<false>& b, unsigned at, int r) {
+    Load in;
+    fetch<0, false>(in, at, b);
+    work(in, b, at, r);
+  }
+  __device__ __forceinline__ void finish(int) const {}
+};
 
+template <typename T, bool VEC>
 __global__ void __launch_bounds__(AW_THREADS) norm_kernel(const __grid_constant__ AwTable tab, double* partial) {
   pdl_wait();
   pdl_trigger();
-  double sum = 0.0;
-  for (unsigned c = blockIdx.x; c < tab.chunks; c += gridDim.x) {
-    const int i = find(tab, c);
-    const AwTensor& t = tab.t[i];
-    Block b;
-    if (!block_of(b, t, c - tab.first[i])) continue;
-    float g[PER];
-    load(g, t.G, t.gt, b);
-    float s = 0.f;
-#pragma unroll
-    for (int j = 0; j < PER; ++j) s = fmaf(g[j], g[j], s);
-    sum += (double)s;
-  }
-  const double s = cta_sum(sum);
+  NormOp<T> op;
+  walk<VEC>(tab, op);
+  const double s = warp_sum(op.sum);
   if (threadIdx.x == 0) partial[blockIdx.x] = s;
 }
 
-__global__ void __launch_bounds__(AW_THREADS) finish_kernel(const __grid_constant__ ClipArgs a) {
+__global__ void __launch_bounds__(FINISH_THREADS) finish_kernel(const __grid_constant__ ClipArgs a) {
+  __shared__ double red[FINISH_THREADS / 32];
   pdl_wait();
   pdl_trigger();
   double sum = 0.0;
-  for (int i = threadIdx.x; i < a.parts; i += AW_THREADS) sum += a.partial[i];
-  const double s = cta_sum(sum);
+  for (int i = threadIdx.x; i < a.parts; i += FINISH_THREADS) sum += a.partial[i];
+  sum = warp_sum(sum);
+  if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = sum;
+  __syncthreads();
   if (threadIdx.x != 0) return;
+  double s = 0.0;
+#pragma unroll
+  for (int k = 0; k < FINISH_THREADS / 32; ++k) s += red[k];
   const float scale = a.scale ? *a.scale : 1.f;
   const float norm = (float)(fabs((double)scale) * sqrt(s));
   const float f = a.max_norm / (norm + 1e-6f);
@@ -440,71 +864,147 @@ __global__ void __launch_bounds__(AW_THREADS) finish_kernel(const __grid_constan
   if (a.nonfinite) *a.nonfinite = isfinite(norm) ? 0 : 1;
 }
 
+template <typename T, typename OUT>
+struct ScaleOp {
+  using Load = Raw<T>;
+  float f;
+  const T* g;
+  OUT* out;
+  __device__ __forceinline__ void start(const AwTensor& t, unsigned long long first, int) {
+    g = static_cast<const T*>(t.G) + first;
+    out = static_cast<OUT*>(t.C) + first;
+  }
+  template <int AT, bool WIDE = true>
+  __device__ __forceinline__ void fetch(Load& in, unsigned at, const Place<WIDE>& b = {}) const { mo::fetch<WIDE, AT>(in, g + at, b); }
+  template <bool WIDE>
+  __device__ __forceinline__ void work(const Load& in, const Place<WIDE>& b, unsigned at, int) const {
+    float x[PER];
+    widen_all(x, in);
+#pragma unroll
+    for (int j = 0; j < PER; ++j) x[j] *= f;
+    store(x, out + at, b);
+  }
+  __device__ __forceinline__ void narrow(const AwTensor&, const Place<false>& b, unsigned at, int r) const {
+    Load in;
+    fetch<0, false>(in, at, b);
+    work(in, b, at, r);
+  }
+  __device__ __forceinline__ void finish(int) const {}
+};
+
+template <typename T, typename OUT, bool VEC>
 __global__ void __launch_bounds__(AW_THREADS) scale_kernel(const __grid_constant__ AwTable tab, const float* factor) {
   pdl_wait();
   pdl_trigger();
-  const float f = *factor;
-  for (unsigned c = blockIdx.x; c < tab.chunks; c += gridDim.x) {
-    const int i = find(tab, c);
-    const AwTensor& t = tab.t[i];
-    Block b;
-    if (!block_of(b, t, c - tab.first[i])) continue;
-    float g[PER];
-    load(g, t.G, t.gt, b);
-#pragma unroll
-    for (int j = 0; j < PER; ++j) g[j] *= f;
-    store(g, t.C, t.ct, b);
-  }
+  ScaleOp<T, OUT> op;
+  op.f = *factor;
+  walk<VEC>(tab, op);
 }
 
-// CTAs of a launch: as many as fit on the card, at most one per chunk.
-unsigned grid_of(unsigned chunks, int per_sm) {
+// CTAs of a launch: as many as fit on the card, at most one per run.
+unsigned grid_of(const AwTable& t, int per_sm) {
   const unsigned most = (unsigned)(device_sm_count() * per_sm);
-  return chunks < most ? chunks : most;
+  return t.runs < most ? t.runs : most;
 }
 
-constexpr int CTAS_PER_SM = 4;
+#ifndef PACK_CTAS
+#define PACK_CTAS 24
+#endif
+#ifndef CPL
+#define CPL 32
+#endif
+
+// Calls f with a null pointer of the element type t.
+template <typename F>
+cudaError_t with_type(AwType t, F f) {
+  if (t == AW_F32) return f(static_cast<float*>(nullptr));
+  if (t == AW_BF16) return f(static_cast<__nv_bfloat16*>(nullptr));
+  return f(static_cast<__half*>(nullptr));
+}
+template <typename F>
+cudaError_t with_wide_type(AwType t, F f) {
+  return t == AW_F32 ? f(static_cast<float*>(nullptr)) : f(static_cast<__nv_bfloat16*>(nullptr));
+}
+template <typename P>
+using Pointee = typename std::remove_pointer<P>::type;
+
+template <typename... KArgs, typename... Args>
+cudaError_t launch_list(void (*kern)(AwTable, KArgs...), int kind, const AwTable& t, unsigned grid, cudaStream_t s,
+                        Args&&... args) {
+  ProfScope prof(kind, s);
+  return launch_pdl(kern, dim3(grid), dim3(AW_THREADS), 0, s, false, t, std::forward<Args>(args)...);
+}
+
+template <bool EIGHT>
+cudaError_t launch_step(const AwTable& t, const AwHyper& h, cudaStream_t s) {
+  return with_wide_type(t.t[0].wt, [&](auto* w) {
+    return with_type(t.t[0].gt, [&](auto* g) {
+      using W = Pointee<decltype(w)>;
+      using G = Pointee<decltype(g)>;
+      return launch_list(t.t[0].vec ? adamw_kernel<EIGHT, W, G, true> : adamw_kernel<EIGHT, W, G, false>, PK_ADAMW, t,
+                         grid_of(t, EIGHT ? STEP8_CTAS : STEP32_CTAS), s, h);
+    });
+  });
+}
 
 }  // namespace
 
-cudaError_t launch_adamw(const AwTable& t, const AwHyper& h, cudaStream_t s) {
-  ProfScope prof(PK_ADAMW, s);
-  return launch_pdl(adamw_kernel<false>, dim3(grid_of(t.chunks, CTAS_PER_SM)), dim3(AW_THREADS), 0, s, false, t, h);
+int run_of(long long blocks) {
+#ifdef RUN
+  return RUN;
+#else
+  const long long warps = (long long)device_sm_count() * STEP8_CTAS;
+  int run = 1;
+  while (run < AW_RUN && blocks >= 8 * run * warps) run *= 2;
+  return run;
+#endif
 }
 
-cudaError_t launch_adamw8(const AwTable& t, const AwHyper& h, cudaStream_t s) {
-  ProfScope prof(PK_ADAMW, s);
-  return launch_pdl(adamw_kernel<true>, dim3(grid_of(t.chunks, CTAS_PER_SM)), dim3(AW_THREADS), 0, s, false, t, h);
-}
+cudaError_t launch_adamw(const AwTable& t, const AwHyper& h, cudaStream_t s) { return launch_step<false>(t, h, s); }
+cudaError_t launch_adamw8(const AwTable& t, const AwHyper& h, cudaStream_t s) { return launch_step<true>(t, h, s); }
 
 cudaError_t launch_pack(const AwTable& t, const AwHyper& h, cudaStream_t s) {
-  ProfScope prof(PK_MOMENTS, s);
-  return launch_pdl(pack_kernel, dim3(grid_of(t.chunks, CTAS_PER_SM)), dim3(AW_THREADS), 0, s, false, t, h);
+  return with_wide_type(t.t[0].gt, [&](auto* m) {
+    using T = Pointee<decltype(m)>;
+    return launch_list(t.t[0].vec ? pack_kernel<T, true> : pack_kernel<T, false>, PK_MOMENTS, t,
+                       grid_of(t, PACK_CTAS), s, h);
+  });
 }
 
 cudaError_t launch_unpack(const AwTable& t, cudaStream_t s) {
-  ProfScope prof(PK_MOMENTS, s);
-  return launch_pdl(unpack_kernel, dim3(grid_of(t.chunks, CTAS_PER_SM)), dim3(AW_THREADS), 0, s, false, t);
+  return with_wide_type(t.t[0].wt, [&](auto* m) {
+    using T = Pointee<decltype(m)>;
+    return launch_list(t.t[0].vec ? unpack_kernel<T, true> : unpack_kernel<T, false>, PK_MOMENTS, t,
+                       grid_of(t, CPL), s);
+  });
 }
 
-int clip_norm_ctas(unsigned chunks, int most) {
-  const unsigned g = grid_of(chunks, CTAS_PER_SM);
+int clip_norm_ctas(const AwTable& t, int most) {
+  const unsigned g = grid_of(t, CPL);
   return (int)(g < (unsigned)most ? g : (unsigned)most);
 }
 
 cudaError_t launch_clip_norm(const AwTable& t, double* partial, int ctas, cudaStream_t s) {
-  ProfScope prof(PK_CLIP, s);
-  return launch_pdl(norm_kernel, dim3(ctas), dim3(AW_THREADS), 0, s, false, t, partial);
+  return with_type(t.t[0].gt, [&](auto* g) {
+    using G = Pointee<decltype(g)>;
+    return launch_list(t.t[0].vec ? norm_kernel<G, true> : norm_kernel<G, false>, PK_CLIP, t, ctas, s, partial);
+  });
 }
 
 cudaError_t launch_clip_finish(const ClipArgs& a, cudaStream_t s) {
   ProfScope prof(PK_CLIP, s);
-  return launch_pdl(finish_kernel, dim3(1), dim3(AW_THREADS), 0, s, false, a);
+  return launch_pdl(finish_kernel, dim3(1), dim3(FINISH_THREADS), 0, s, false, a);
 }
 
 cudaError_t launch_clip_scale(const AwTable& t, const float* factor, cudaStream_t s) {
-  ProfScope prof(PK_CLIP, s);
-  return launch_pdl(scale_kernel, dim3(grid_of(t.chunks, CTAS_PER_SM)), dim3(AW_THREADS), 0, s, false, t, factor);
+  return with_type(t.t[0].gt, [&](auto* g) {
+    return with_type(t.t[0].ct, [&](auto* o) {
+      using G = Pointee<decltype(g)>;
+      using O = Pointee<decltype(o)>;
+      return launch_list(t.t[0].vec ? scale_kernel<G, O, true> : scale_kernel<G, O, false>, PK_CLIP, t,
+                         grid_of(t, CPL), s, factor);
+    });
+  });
 }
 
 }  // namespace mo

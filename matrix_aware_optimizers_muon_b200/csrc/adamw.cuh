@@ -10,13 +10,14 @@
 namespace mo {
 
 constexpr int AW_BLOCK = 256;      // elements that share a scale of the 8-bit moments
-constexpr int AW_THREADS = 256;    // 8 warps, one 256-element block each
-constexpr int AW_CHUNK = AW_BLOCK * (AW_THREADS / 32);   // elements of one CTA pass
+constexpr int AW_THREADS = 32;     // a CTA is one warp, which works on one block at a time
+constexpr int AW_RUN = 32;         // most blocks of a run: their scales are one 32-byte sector
 constexpr int AW_MAX = 320;        // tensors per launch (the table travels in the kernel's parameters)
 
 enum AwType : unsigned char { AW_F32 = 0, AW_BF16 = 1, AW_F16 = 2, AW_NONE = 3 };
 
-// One tensor.  Which pointers are used depends on the kernel:
+// One tensor.  All tensors of a table have the types and the alignment (vec) of
+// the first.  Which pointers are used depends on the kernel:
 //   adamw    W, G, M, V (fp32), C (optional low-precision copy of W)
 //   adamw8   W, G, M, V (codes), MS, VS (scales), C
 //   pack     G = first moment, C = second moment (read), M, V, MS, VS (written)
@@ -39,8 +40,9 @@ struct AwTensor {
 
 struct AwTable {
   int n;
-  unsigned chunks;                 // first[n]
-  unsigned first[AW_MAX + 1];      // first chunk of each tensor
+  int run;                         // blocks of a run, the work that a CTA takes at a time
+  unsigned runs;                   // first[n]
+  unsigned first[AW_MAX + 1];      // first run of each tensor
   AwTensor t[AW_MAX];
 };
 
@@ -70,12 +72,14 @@ struct ClipArgs {
 
 constexpr int CLIP_MAX_CTAS = 8192;   // partial sums of one call
 
+// Blocks of a run (at most AW_RUN) for a list of so many blocks.
+int run_of(long long blocks);
 cudaError_t launch_adamw(const AwTable& t, const AwHyper& h, cudaStream_t s);
 cudaError_t launch_adamw8(const AwTable& t, const AwHyper& h, cudaStream_t s);
 cudaError_t launch_pack(const AwTable& t, const AwHyper& h, cudaStream_t s);
 cudaError_t launch_unpack(const AwTable& t, cudaStream_t s);
-// CTAs of the norm launch over `chunks` chunks (its number of partial sums), at most `most`
-int clip_norm_ctas(unsigned chunks, int most);
+// CTAs of the norm launch (its number of partial sums), at most `most`
+int clip_norm_ctas(const AwTable& t, int most);
 cudaError_t launch_clip_norm(const AwTable& t, double* partial, int ctas, cudaStream_t s);
 cudaError_t launch_clip_finish(const ClipArgs& a, cudaStream_t s);
 cudaError_t launch_clip_scale(const AwTable& t, const float* factor, cudaStream_t s);

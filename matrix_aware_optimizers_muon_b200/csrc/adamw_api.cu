@@ -21,7 +21,7 @@ mo_status ctx_fail(mo_ctx* ctx, mo_status st, const std::string& msg);
 
 namespace {
 
-constexpr int64_t MAX_NUMEL = (int64_t)1 << 40;
+constexpr int64_t MAX_NUMEL = (int64_t)1 << 38;   // blocks count in 31 bits
 
 bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 size_t width(int type) { return type == AW_F32 ? 4 : 2; }
@@ -74,26 +74,43 @@ bool numel_ok(int64_t numel, int i) {
 
 size_t blocks_of(int64_t numel) { return (size_t)((numel + AW_BLOCK - 1) / AW_BLOCK); }
 
-// Splits the list into launches of at most AW_MAX tensors.
+// Splits the list into launches of one set of types, of aligned tensors or of
+// others, and of at most AW_MAX tensors.
 class Tables {
  public:
-  void add(AwTensor t) {
-    const long long chunks = (t.numel + AW_CHUNK - 1) / AW_CHUNK;
-    if (tabs_.empty() || tabs_.back().n == AW_MAX || tabs_.back().chunks + chunks > 0x7fffffffll) {
+  explicit Tables(bool by_output = false) : by_output_(by_output) { std::fill_n(&open_[0][0][0], 2 * 4 * 4, -1); }
+  void add(const AwTensor& t) {
+    // clip_grads leaves wt alone and launches by the output's type instead
+    int& open = open_[t.vec][by_output_ ? t.ct : t.wt][t.gt];
+    const long long blocks = (long long)blocks_of(t.numel);
+    if (open < 0 || tabs_[open].n == AW_MAX || blocks_[open] + blocks > MAX_BLOCKS) {
+      open = (int)tabs_.size();
       tabs_.emplace_back();
       tabs_.back().n = 0;
-      tabs_.back().chunks = 0;
-      tabs_.back().first[0] = 0;
+      blocks_.push_back(0);
     }
-    AwTable& tab = tabs_.back();
-    tab.t[tab.n++] = t;
-    tab.chunks += (unsigned)chunks;
-    tab.first[tab.n] = tab.chunks;
+    tabs_[open].t[tabs_[open].n++] = t;
+    blocks_[open] += blocks;
+  }
+  // Divides the tensors into runs, once all are in.
+  void finish() {
+    for (size_t k = 0; k < tabs_.size(); ++k) {
+      AwTable& tab = tabs_[k];
+      tab.run = run_of(blocks_[k]);
+      tab.first[0] = 0;
+      for (int i = 0; i < tab.n; ++i)
+        tab.first[i + 1] = tab.first[i] + (unsigned)((blocks_of(tab.t[i].numel) + tab.run - 1) / tab.run);
+      tab.runs = tab.first[tab.n];
+    }
   }
   const std::vector<AwTable>& all() const { return tabs_; }
 
  private:
+  static constexpr long long MAX_BLOCKS = 0x7fffffffll;
   std::vector<AwTable> tabs_;
+  std::vector<long long> blocks_;
+  int open_[2][4][4];              // the table that takes the next such tensor
+  bool by_output_;
 };
 
 bool finite_nonneg(double x) { return std::isfinite(x) && x >= 0.0; }
@@ -241,6 +258,7 @@ mo_status adamw_step(mo_ctx* ctx, const mo_adamw_tensor* list, int n, const mo_a
       tabs.add(t);
     }
     check_apart(r);
+    tabs.finish();
     return launch([&]() {
       cudaError_t e = cudaSuccess;
       for (const AwTable& tab : tabs.all())
@@ -270,6 +288,7 @@ mo_status adamw8_step(mo_ctx* ctx, const mo_adamw8_tensor* list, int n, const mo
       tabs.add(t);
     }
     check_apart(r);
+    tabs.finish();
     return launch([&]() {
       cudaError_t e = cudaSuccess;
       for (const AwTable& tab : tabs.all())
@@ -310,6 +329,7 @@ mo_status adamw8_pack(mo_ctx* ctx, const mo_adamw8_moments* list, int n, const m
       tabs.add(t);
     }
     check_apart(r);
+    tabs.finish();
     return launch([&]() {
       cudaError_t e = cudaSuccess;
       for (const AwTable& tab : tabs.all())
@@ -344,6 +364,7 @@ mo_status adamw8_unpack(mo_ctx* ctx, const mo_adamw8_moments* list, int n, void*
       tabs.add(t);
     }
     check_apart(r);
+    tabs.finish();
     return launch([&]() {
       cudaError_t e = cudaSuccess;
       for (const AwTable& tab : tabs.all())
@@ -372,7 +393,7 @@ mo_status clip_grads(mo_ctx* ctx, const mo_grad* list, int n, const mo_clip_cfg*
     add(r, cfg->factor, 4, true);
     add(r, cfg->nonfinite, 4, true);
     add(r, cfg->scale, 4, false);
-    Tables tabs;
+    Tables tabs(true);
     for (int i = 0; i < n; ++i) {
       const mo_grad& a = list[i];
       if (!numel_ok(a.numel, i) || a.G == nullptr) continue;
@@ -397,6 +418,7 @@ mo_status clip_grads(mo_ctx* ctx, const mo_grad* list, int n, const mo_clip_cfg*
       tabs.add(t);
     }
     check_apart(r);
+    tabs.finish();
     size_t ws_bytes = 0;
     char* ws = ctx_workspace(ctx, &ws_bytes);
     if (ws == nullptr || ws_bytes < MO_CLIP_WORKSPACE_BYTES)
@@ -416,7 +438,7 @@ mo_status clip_grads(mo_ctx* ctx, const mo_grad* list, int n, const mo_clip_cfg*
       cudaError_t e = cudaSuccess;
       for (const AwTable& tab : tabs.all()) {
         if (e != cudaSuccess) break;
-        const int ctas = clip_norm_ctas(tab.chunks, each);
+        const int ctas = clip_norm_ctas(tab, each);
         e = launch_clip_norm(tab, a.partial + a.parts, ctas, s);
         a.parts += ctas;
       }

@@ -66,7 +66,7 @@ def test_bad_hyperparameters(lib, ctx, make, kw, word):
 
 @pytest.mark.parametrize("make", [_tensor, _tensor8])
 @pytest.mark.parametrize("kw,word", [
-    (dict(numel=-1), "numel"), (dict(numel=(1 << 40) + 1), "numel"), (dict(W=None), "null W"), (dict(W=(1 << 20) + 2), "W must be aligned"),
+    (dict(numel=-1), "numel"), (dict(numel=(1 << 38) + 1), "numel"), (dict(W=None), "null W"), (dict(W=(1 << 20) + 2), "W must be aligned"),
     (dict(G=(2 << 20) + 1, g_type=1), "G must be aligned"), (dict(w_type=2), "w_type"), (dict(w_type=3), "w_type"),
     (dict(g_type=-1), "g_type"), (dict(lr_scale=-1.0), "lr_scale"), (dict(weight_decay=float("nan")), "weight_decay"),
     (dict(copy=7 << 20, copy_type=0), "copy"), (dict(copy=7 << 20, copy_type=1, w_type=1), "copy"),
