@@ -352,7 +352,7 @@ MO_API mo_status mo_soap_muon_workspace_bytes(mo_ctx* ctx, const mo_soap_muon_ma
  *   V <- b2 V + (1 - b2) g * g
  *   W <- (1 - lr' wd) W - lr' (M / (1 - b1^t)) / (sqrt(V / (1 - b2^t)) + eps)
  * with lr' = lr * lr_scale and wd = weight_decay of the tensor.  The whole list
- * takes one launch for each 320 tensors and no workspace.
+ * takes one launch for each 350 tensors of one pair of types and no workspace.
  *  - A tensor is numel contiguous elements at a pointer aligned to its
  *    element; numel 0 or G == NULL skips it.  The wide path needs pointers
  *    aligned to 8 elements (8-bit codes to 8 bytes) and gives the same bits.
@@ -499,6 +499,30 @@ typedef struct {
 
 MO_API mo_status clip_grads(mo_ctx* ctx, const mo_grad* list /* host array */, int n, const mo_clip_cfg* cfg,
                             void* stream);
+
+/* ------------------------------------------------------------------ prepared lists
+ * The lists of the four kinds of calls above, checked and laid out once: a
+ * program whose parameters, gradients and state stay in place makes one and
+ * passes it to every step (the checks and tables of 300 tensors take the host
+ * some 30 us, a step with a prepared list 4).  A list holds addresses and
+ * sizes, in host memory, and no contents.  A moments list serves adamw8_pack
+ * and adamw8_unpack.  Results and refusals are those of the calls with arrays;
+ * *out is NULL after a refusal.  mo_list_destroy takes NULL. */
+typedef struct mo_list mo_list;
+
+MO_API mo_status mo_adamw_list(mo_ctx* ctx, const mo_adamw_tensor* list, int n, mo_list** out);
+MO_API mo_status mo_adamw8_list(mo_ctx* ctx, const mo_adamw8_tensor* list, int n, mo_list** out);
+MO_API mo_status mo_moments_list(mo_ctx* ctx, const mo_adamw8_moments* list, int n, mo_list** out);
+MO_API mo_status mo_grad_list(mo_ctx* ctx, const mo_grad* list, int n, mo_list** out);
+MO_API void mo_list_destroy(mo_list* list);
+
+MO_API mo_status adamw_step_list(mo_ctx* ctx, const mo_list* list, const mo_adamw_cfg* cfg, int64_t step,
+                                 void* stream);
+MO_API mo_status adamw8_step_list(mo_ctx* ctx, const mo_list* list, const mo_adamw_cfg* cfg, int64_t step,
+                                  void* stream);
+MO_API mo_status adamw8_pack_list(mo_ctx* ctx, const mo_list* list, const mo_pack_cfg* cfg, void* stream);
+MO_API mo_status adamw8_unpack_list(mo_ctx* ctx, const mo_list* list, void* stream);
+MO_API mo_status clip_grads_list(mo_ctx* ctx, const mo_list* list, const mo_clip_cfg* cfg, void* stream);
 
 /* ------------------------------------------------------------------ building block
  * The batched tensor-core GEMM the steps are built from, exposed for tests

@@ -30,6 +30,10 @@ def _ptr(t):
     return None if t is None else c_void_p(t.data_ptr())
 
 
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
 def _check_f32(t, name):
     import torch
     if t is None:
@@ -70,17 +74,21 @@ def _check_extent(t, name, rows, cols, ld, stride, batch, dtypes):
                          f"needs {last} elements, the tensor has {t.numel()}")
 
 
+_TYPES = {}      # torch dtype -> the library's type, and whether a check allows it (filled on first use)
+
+
 def _type(t, name, i, device, types):
     """The library's type of a flat tensor, checked: the library gets pointers only."""
-    import torch
-    codes = {torch.float32: _lib.F32, torch.bfloat16: _lib.BF16, torch.float16: _lib.F16, torch.uint8: None}
-    allowed = [{"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16, "u8": torch.uint8}[k]
-               for k in types]
-    if t.dtype not in allowed or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"tensor {i}: {name} must be a contiguous CUDA tensor of dtype {allowed}")
+    if not _TYPES:
+        import torch
+        _TYPES.update({torch.float32: (_lib.F32, "f32"), torch.bfloat16: (_lib.BF16, "bf16"),
+                       torch.float16: (_lib.F16, "f16"), torch.uint8: (None, "u8")})
+    code, kind = _TYPES.get(t.dtype, (None, ""))
+    if kind not in types or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"tensor {i}: {name} must be a contiguous CUDA tensor of type {' or '.join(types)}")
     if t.device.index != device:
         raise ValueError(f"tensor {i}: {name} is on {t.device}, the context on cuda:{device}")
-    return codes[t.dtype]
+    return code
 
 
 def _same_numel(t, name, i, numel):
@@ -100,18 +108,24 @@ def _scalar(t, name, device, dtype):
 
 
 class TensorList:
-    """A checked list for adamw_step, adamw8_step, adamw8_pack / adamw8_unpack or clip_grads.
+    """A prepared list for adamw_step, adamw8_step, adamw8_pack / adamw8_unpack or clip_grads.
 
-    A program that keeps its parameters, gradients and state in place makes
-    it once and passes it to every step; it holds the tensors.  Made by
-    Context.adamw_tensors, adamw8_tensors, adamw8_moments and clip_tensors."""
+    The library's checks and launch tables of a list whose tensors stay in
+    place, for a program that makes it once and passes it to every step.  It
+    holds the tensors.  Made by Context.adamw_tensors, adamw8_tensors,
+    adamw8_moments and clip_tensors."""
 
-    def __init__(self, kind, array, n, tensors, device):
-        self.kind, self.array, self.n, self.device = kind, array, n, device
-        self.tensors = tensors
+    def __init__(self, kind, lib, handle, tensors, device):
+        self.kind, self.lib, self.handle, self.tensors, self.device = kind, lib, handle, tensors, device
 
     def __len__(self):
-        return self.n
+        return len(self.tensors)
+
+    def __del__(self):
+        try:
+            self.lib.mo_list_destroy(self.handle)
+        except Exception:
+            pass
 
 
 class Context:
@@ -383,6 +397,11 @@ class Context:
                                             self._stream(stream)))
 
     # ------------------------------------------------------------ AdamW, clipping
+    def _prepare(self, kind, make, array, tensors):
+        h = c_void_p()
+        self._check(make(self.handle, array, len(tensors), byref(h)))
+        return TensorList(kind, self.lib, h, tensors, self.device)
+
     def _list(self, kind, mats):
         """mats as a TensorList of this kind."""
         if not isinstance(mats, TensorList):
@@ -393,8 +412,8 @@ class Context:
                              f"this one is for {mats.kind!r} on cuda:{mats.device}")
         return mats
 
-    def _step_fields(self, i, d, state, keep):
-        """What both kinds of AdamW tensors share: (numel, pointers, types, lr_scale, weight_decay)."""
+    def _step_fields(self, i, d):
+        """What both kinds of AdamW tensors share."""
         W, G, copy = d["W"], d.get("G"), d.get("copy")
         n = W.numel()
         wt = _type(W, "W", i, self.device, ("f32", "bf16"))
@@ -405,8 +424,7 @@ class Context:
         if copy is not None:
             ct = _type(copy, "copy", i, self.device, ("bf16", "f16"))
             _same_numel(copy, "copy", i, n)
-        keep.append((W, G, copy, *state))
-        return n, W, G, copy, wt, gt, ct, d.get("lr_scale", 1.0), d.get("weight_decay", 0.0)
+        return n, W, G, copy, (wt, gt, ct, d.get("lr_scale", 1.0), d.get("weight_decay", 0.0))
 
     def adamw_tensors(self, mats):
         """The list for adamw_step: dicts with W, G (None: skipped), M, V (fp32)
@@ -414,15 +432,16 @@ class Context:
         arr, keep = (AdamWTensor * max(len(mats), 1))(), []
         for i, d in enumerate(mats):
             M, V = d["M"], d["V"]
-            n, W, G, copy, wt, gt, ct, ls, wd = self._step_fields(i, d, (M, V), keep)
+            n, W, G, copy, rest = self._step_fields(i, d)
             for t, nm in ((M, "M"), (V, "V")):
                 _type(t, nm, i, self.device, ("f32",))
                 _same_numel(t, nm, i, n)
-            arr[i] = AdamWTensor(n, _ptr(W), _ptr(G), _ptr(M), _ptr(V), _ptr(copy), wt, gt, ct, ls, wd)
-        return TensorList("adamw", arr, len(mats), keep, self.device)
+            keep.append((W, G, M, V, copy))
+            arr[i] = AdamWTensor(n, _addr(W), _addr(G), _addr(M), _addr(V), _addr(copy), *rest)
+        return self._prepare("adamw", self.lib.mo_adamw_list, arr, keep)
 
     def _codes(self, i, d, n):
-        codes = [d[k] for k in ("M8", "V8", "MS", "VS")]
+        codes = [d["M8"], d["V8"], d["MS"], d["VS"]]
         for t, nm, size in zip(codes, ("M8", "V8", "MS", "VS"), (n, n, -(-n // 256), -(-n // 256))):
             _type(t, nm, i, self.device, ("u8",))
             _same_numel(t, nm, i, size)
@@ -434,10 +453,11 @@ class Context:
         each 256 elements) in the place of M and V."""
         arr, keep = (AdamW8Tensor * max(len(mats), 1))(), []
         for i, d in enumerate(mats):
-            codes = self._codes(i, d, d["W"].numel())
-            n, W, G, copy, wt, gt, ct, ls, wd = self._step_fields(i, d, codes, keep)
-            arr[i] = AdamW8Tensor(n, _ptr(W), _ptr(G), *map(_ptr, codes), _ptr(copy), wt, gt, ct, ls, wd)
-        return TensorList("adamw8", arr, len(mats), keep, self.device)
+            n, W, G, copy, rest = self._step_fields(i, d)
+            codes = self._codes(i, d, n)
+            keep.append((W, G, copy, *codes))
+            arr[i] = AdamW8Tensor(n, _addr(W), _addr(G), *map(_addr, codes), _addr(copy), *rest)
+        return self._prepare("adamw8", self.lib.mo_adamw8_list, arr, keep)
 
     def adamw8_state(self, W):
         """Zero 8-bit moments for the parameter W: a dict of M8, V8, MS and VS."""
@@ -459,8 +479,8 @@ class Context:
                 raise ValueError(f"tensor {i}: M and V must have one dtype")
             codes = self._codes(i, d, n)
             keep.append((M, V, *codes))
-            arr[i] = AdamW8Moments(n, *map(_ptr, codes), _ptr(M), _ptr(V), types[0])
-        return TensorList("moments", arr, len(mats), keep, self.device)
+            arr[i] = AdamW8Moments(n, *map(_addr, codes), _addr(M), _addr(V), types[0])
+        return self._prepare("moments", self.lib.mo_moments_list, arr, keep)
 
     def clip_tensors(self, grads):
         """The list for clip_grads: gradients, or dicts with G and out (None:
@@ -469,15 +489,15 @@ class Context:
         types = ("f32", "bf16", "f16")
         for i, d in enumerate(grads):
             G, out = (d["G"], d.get("out")) if isinstance(d, dict) else (d, None)
+            keep.append((G, out))
             if G is None:
                 continue
             gt = ot = _type(G, "G", i, self.device, types)
             if out is not None:
                 ot = _type(out, "out", i, self.device, types)
                 _same_numel(out, "out", i, G.numel())
-            keep.append((G, out))
-            arr[i] = Grad(G.numel(), _ptr(G), _ptr(out), gt, ot)
-        return TensorList("grads", arr, len(grads), keep, self.device)
+            arr[i] = Grad(G.numel(), _addr(G), _addr(out), gt, ot)
+        return self._prepare("grads", self.lib.mo_grad_list, arr, keep)
 
     def _adamw(self, fn, mats, step, lr, beta1, beta2, eps, bias_correction, grad_scale, skip, seed, stream):
         import torch
@@ -486,10 +506,10 @@ class Context:
             step, step_dev = 1, _scalar(step, "step", self.device, torch.int64)
         if isinstance(lr, torch.Tensor):
             lr, lr_dev = 0.0, _scalar(lr, "lr", self.device, torch.float32)
-        cfg = AdamWCfg(lr, beta1, beta2, eps, int(bias_correction), int(seed is not None), seed or 0, lr_dev, step_dev,
+        cfg = AdamWCfg(lr, beta1, beta2, eps, bool(bias_correction), seed is not None, seed or 0, lr_dev, step_dev,
                        _scalar(grad_scale, "grad_scale", self.device, torch.float32),
                        _scalar(skip, "skip", self.device, torch.int32))
-        self._check(fn(self.handle, mats.array, mats.n, byref(cfg), int(step), self._stream(stream)))
+        self._check(fn(self.handle, mats.handle, cfg, int(step), self._stream(stream)))
 
     def adamw_step(self, mats, step, *, lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, bias_correction=True,
                    grad_scale=None, skip=None, seed=None, stream=None):
@@ -499,8 +519,8 @@ class Context:
         read when the kernel runs.  ``grad_scale`` (fp32) multiplies every
         gradient, a nonzero ``skip`` (int32) leaves everything as it is.  With a
         ``seed`` bf16 weights are rounded stochastically, else to nearest."""
-        self._adamw(self.lib.adamw_step, self._list("adamw", mats), step, lr, beta1, beta2, eps, bias_correction,
-                    grad_scale, skip, seed, stream)
+        self._adamw(self.lib.adamw_step_list, self._list("adamw", mats), step, lr, beta1, beta2, eps,
+                    bias_correction, grad_scale, skip, seed, stream)
 
     def adamw8_step(self, mats, step, *, lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, bias_correction=True,
                     grad_scale=None, skip=None, seed=0, stream=None):
@@ -508,8 +528,8 @@ class Context:
         it takes).  With a ``seed`` the second moment and bf16 weights are
         rounded stochastically; None rounds to nearest, which leaves a slowly
         changing second moment where it is.  The rest is as in adamw_step."""
-        self._adamw(self.lib.adamw8_step, self._list("adamw8", mats), step, lr, beta1, beta2, eps, bias_correction,
-                    grad_scale, skip, seed, stream)
+        self._adamw(self.lib.adamw8_step_list, self._list("adamw8", mats), step, lr, beta1, beta2, eps,
+                    bias_correction, grad_scale, skip, seed, stream)
 
     def adamw8_pack(self, mats, *, seed=None, step=0, stream=None):
         """Moments M, V to 8-bit codes (adamw8_moments, or what it takes); with a
@@ -519,13 +539,13 @@ class Context:
         step_dev = None
         if isinstance(step, torch.Tensor):
             step, step_dev = 0, _scalar(step, "step", self.device, torch.int64)
-        cfg = PackCfg(int(seed is not None), seed or 0, int(step), step_dev)
-        self._check(self.lib.adamw8_pack(self.handle, mats.array, mats.n, byref(cfg), self._stream(stream)))
+        cfg = PackCfg(seed is not None, seed or 0, int(step), step_dev)
+        self._check(self.lib.adamw8_pack_list(self.handle, mats.handle, cfg, self._stream(stream)))
 
     def adamw8_unpack(self, mats, *, stream=None):
         """The values that 8-bit codes stand for, written to M and V."""
         mats = self._list("moments", mats)
-        self._check(self.lib.adamw8_unpack(self.handle, mats.array, mats.n, self._stream(stream)))
+        self._check(self.lib.adamw8_unpack_list(self.handle, mats.handle, self._stream(stream)))
 
     def clip_grads(self, grads, max_norm, *, apply=True, scale=None, nonfinite=None, stream=None, reserve=True):
         """Scales the gradients of a list (clip_tensors, or what it takes) so that
@@ -536,14 +556,14 @@ class Context:
         receives 1 when the norm is not finite."""
         import torch
         grads = self._list("grads", grads)
-        if reserve and (self.workspace is None or self.workspace.numel() < _lib.CLIP_WORKSPACE_BYTES):
+        if reserve and (self._workspace is None or self._workspace.numel() < _lib.CLIP_WORKSPACE_BYTES):
             self.attach_workspace(_lib.CLIP_WORKSPACE_BYTES, stream)
         with torch.cuda.stream(stream):     # the scalars belong to the stream that writes them
-            out = torch.empty(2, dtype=torch.float32, device=f"cuda:{self.device}")
-        norm, factor = out[0], out[1]
-        cfg = ClipCfg(max_norm, int(apply), _scalar(scale, "scale", self.device, torch.float32), norm.data_ptr(),
-                      factor.data_ptr(), _scalar(nonfinite, "nonfinite", self.device, torch.int32))
-        self._check(self.lib.clip_grads(self.handle, grads.array, grads.n, byref(cfg), self._stream(stream)))
+            norm, factor = torch.empty(2, dtype=torch.float32, device=f"cuda:{self.device}").unbind()
+        at = norm.data_ptr()
+        cfg = ClipCfg(max_norm, bool(apply), _scalar(scale, "scale", self.device, torch.float32), at, at + 4,
+                      _scalar(nonfinite, "nonfinite", self.device, torch.int32))
+        self._check(self.lib.clip_grads_list(self.handle, grads.handle, cfg, self._stream(stream)))
         return norm, factor
 
     def gemm_bf16(self, A, B, D, *, M, N, K, batch=1, a_mn=False, b_mn=False, sym=False,

@@ -159,6 +159,16 @@ SIGNATURES = {
     "adamw8_pack": (c_int, [c_void_p, POINTER(AdamW8Moments), c_int, POINTER(PackCfg), c_void_p]),
     "adamw8_unpack": (c_int, [c_void_p, POINTER(AdamW8Moments), c_int, c_void_p]),
     "clip_grads": (c_int, [c_void_p, POINTER(Grad), c_int, POINTER(ClipCfg), c_void_p]),
+    "mo_adamw_list": (c_int, [c_void_p, POINTER(AdamWTensor), c_int, POINTER(c_void_p)]),
+    "mo_adamw8_list": (c_int, [c_void_p, POINTER(AdamW8Tensor), c_int, POINTER(c_void_p)]),
+    "mo_moments_list": (c_int, [c_void_p, POINTER(AdamW8Moments), c_int, POINTER(c_void_p)]),
+    "mo_grad_list": (c_int, [c_void_p, POINTER(Grad), c_int, POINTER(c_void_p)]),
+    "mo_list_destroy": (None, [c_void_p]),
+    "adamw_step_list": (c_int, [c_void_p, c_void_p, POINTER(AdamWCfg), c_int64, c_void_p]),
+    "adamw8_step_list": (c_int, [c_void_p, c_void_p, POINTER(AdamWCfg), c_int64, c_void_p]),
+    "adamw8_pack_list": (c_int, [c_void_p, c_void_p, POINTER(PackCfg), c_void_p]),
+    "adamw8_unpack_list": (c_int, [c_void_p, c_void_p, c_void_p]),
+    "clip_grads_list": (c_int, [c_void_p, c_void_p, POINTER(ClipCfg), c_void_p]),
     "mo_profile_enable": (c_int, [c_void_p, c_int]),
     "mo_profile_read": (c_int, [c_void_p, POINTER(ctypes.c_double), POINTER(ctypes.c_double),
                                 POINTER(c_int64), c_int]),

@@ -28,13 +28,11 @@ namespace mo {
 
 namespace {
 
-#ifndef STEP8_CTAS
-#define STEP8_CTAS 24
-#endif
-#ifndef STEP32_CTAS
-#define STEP32_CTAS 24
-#endif
 constexpr int PER = AW_BLOCK / 32;     // elements of a lane
+// CTAs (warps) of a step on one SM: five for each of its four schedulers, at 96
+// registers.  16 and 24 take 7 and 8 % longer, 21 as long as 24 would: a
+// scheduler with one warp more than the others finishes last.
+constexpr int STEP_CTAS = 20;
 
 // A lane's place in a block: wide lanes hold 8 neighbours, narrow ones elements
 // 32 apart.
@@ -44,6 +42,14 @@ struct Place {
   int left;                   // narrow: elements of the tensor from there on
   __device__ __forceinline__ bool has(int j) const { return WIDE || 32 * j < left; }
 };
+
+// Conditions that hold for few blocks: their code goes out of the way.
+__device__ __forceinline__ bool rare(bool x) { return __builtin_expect(x, 0); }
+
+__device__ __forceinline__ void scale_all(float (&x)[PER], float f) {
+#pragma unroll
+  for (int j = 0; j < PER; ++j) x[j] *= f;
+}
 
 // ---------------------------------------------------------------- loads and stores
 using Code = unsigned char;            // of an 8-bit moment
@@ -175,38 +181,63 @@ __device__ __forceinline__ void store(const float (&x)[PER], T* p, const Place<W
 
 // ---------------------------------------------------------------- the list
 // Tensor that holds run `run` of the list, none before tensor i.
-__device__ __forceinline__ int find(const AwTable& tab, unsigned run, int i) {
-  if (run < tab.first[i + 1]) return i;
+template <int N>
+__device__ __forceinline__ int find(const AwTableOf<N>& tab, unsigned run, int i) {
+  if (i + 1 == tab.n || run < tab.t[i + 1].first) return i;
   int lo = i + 1, hi = tab.n - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (tab.first[mid] <= run) lo = mid; else hi = mid - 1;
+    if (tab.t[mid].first <= run) lo = mid; else hi = mid - 1;
   }
   return lo;
 }
 
+template <typename Op, int... K>
+__device__ __forceinline__ void fetch_all(const Op& op, typename Op::Load (&in)[sizeof...(K)], unsigned at,
+                                          std::integer_sequence<int, K...>) {
+  (op.template fetch<K>(in[K], at), ...);
+}
+
 // A CTA is one warp.  It takes every gridDim-th run of tab.run blocks of a
-// tensor and fetches a block while it works on the one before.
+// tensor.  With BATCH 0 it fetches a block while it works on the one before,
+// else it fetches BATCH blocks and then works on them.
 //   Op::start(tensor, first element, blocks)   a run begins
 //   Op::fetch<AT>(Load&, at)                   reads a whole block, AT blocks behind the lane's offset `at`
 //   Op::work(Load, Place, at, r)               works on block r of the run
 //   Op::narrow(tensor, Place, at, r)           reads and works on block r of a misaligned tensor (VEC false) or a partial one
 //   Op::finish(blocks)                         the run ends
-template <bool VEC, typename Op>
-__device__ __forceinline__ void walk(const AwTable& tab, Op& op) {
+template <bool VEC, int N, typename Op>
+__device__ __forceinline__ void walk(const AwTableOf<N>& tab, Op& op) {
   const unsigned lane = threadIdx.x;
   int i = 0;
-  for (unsigned run = blockIdx.x; run < tab.runs; run += gridDim.x) {
-    i = find(tab, run, i);
+  for (unsigned turn = blockIdx.x; turn < tab.runs; turn += gridDim.x) {
+    const unsigned run = Op::BACKWARDS ? tab.runs - 1 - turn : turn;
+    i = find(tab, run, Op::BACKWARDS ? 0 : i);
     const AwTensor& t = tab.t[i];
-    const long long block = (long long)(run - tab.first[i]) * tab.run;
+    const long long block = (long long)(run - t.first) * tab.run;
     const unsigned long long first = (unsigned long long)block * AW_BLOCK;
     const int blocks = (int)min((long long)tab.run, (t.numel + AW_BLOCK - 1) / AW_BLOCK - block);
     const int whole = VEC ? (int)min((long long)blocks, t.numel / AW_BLOCK - block) : 0;
     op.start(t, first, blocks);
     int r = 0;
-    if (whole > 0) {
-      unsigned at = lane * PER;
+    unsigned at = lane * PER;
+    if constexpr (Op::BATCH > 0) {
+      for (; r + Op::BATCH <= whole; r += Op::BATCH) {
+        typename Op::Load in[Op::BATCH];
+        fetch_all(op, in, at, std::make_integer_sequence<int, Op::BATCH>());
+#pragma unroll
+        for (int k = 0; k < Op::BATCH; ++k) {
+          op.work(in[k], Place<true>{first + at, 0}, at, r + k);
+          at += AW_BLOCK;
+        }
+      }
+      for (; r < whole; ++r) {
+        typename Op::Load in;
+        op.template fetch<0>(in, at);
+        op.work(in, Place<true>{first + at, 0}, at, r);
+        at += AW_BLOCK;
+      }
+    } else if (whole > 0) {
       typename Op::Load even, odd;             // two buffers and two copies of the body: no moves between them
       op.template fetch<0>(even, at);
       while (true) {
@@ -240,7 +271,6 @@ struct Keys {
 };
 
 __device__ __forceinline__ Keys keys_of(const AwHyper& h, unsigned index) {
-  if (!h.stochastic) return {0, 0};
   const unsigned long long step = (unsigned long long)(h.step_dev ? *h.step_dev : h.step);
   unsigned long long z = h.seed + step * 0x9E3779B97F4A7C15ull + index * 0xBB67AE8584CAA73Bull;
 #pragma unroll
@@ -338,7 +368,7 @@ __device__ __forceinline__ void decode(float (&m)[PER], float (&v)[PER], const R
     v[2 * q] = f.x;
     v[2 * q + 1] = f.y;
   }
-  if (has_high(vc.w[0]) || has_high(vc.w[1])) {
+  if (rare(has_high(vc.w[0]) || has_high(vc.w[1]))) {
     // 248 is 2^16, which a block's largest value may round up to; 255 is a NaN
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
@@ -385,7 +415,7 @@ __device__ __forceinline__ void second_codes(unsigned (&r)[PER], const float (&v
     r[j] = STOCHASTIC ? u * 16u + n.bits24(j) : (u + 0x7ffffu + ((u >> 20) & 1u)) * 16u;
     least = min(least, r[j]);
   }
-  if (least < (1u << 24)) {
+  if (rare(least < (1u << 24))) {
 #pragma unroll
     for (int j = 0; j < PER; ++j)
       if (v[j] > 0.f && r[j] < (1u << 24)) r[j] = 1u << 24;
@@ -407,12 +437,13 @@ __device__ __forceinline__ void store_moments(float (&m)[PER], float (&v)[PER], 
   unsigned odd = 0;                                    // elements whose v has code 255
   float scaled[PER];
   unsigned ms, vs;
-  if (um < INF_BITS && uv < HIGH_BITS) {
+  if (!rare(um >= INF_BITS || uv >= HIGH_BITS)) {
     ms = max(1, (int)(um >> 23) - 7);
     vs = max(1, (int)(uv >> 23) - 15);
     const float vi = __uint_as_float((142u - vs) << 23);   // 2^(127 - s) 2^-112, a normal number below HIGH_BITS
 #pragma unroll
-    for (int j = 0; j < PER; ++j) scaled[j] = v[j] * vi;
+    for (int j = 0; j < PER; ++j) scaled[j] = v[j];
+    scale_all(scaled, vi);
   } else {
     // the scale is that of the finite values; an infinite m has no code and becomes a NaN
     um = uv = 0;
@@ -430,14 +461,14 @@ __device__ __forceinline__ void store_moments(float (&m)[PER], float (&v)[PER], 
 #pragma unroll
     for (int j = 0; j < PER; ++j) scaled[j] = v[j] * __uint_as_float((254u - vs) << 23) * 0x1p-112f;
   }
-  const float mi = __uint_as_float((254u - ms) << 23);
+  scale_all(m, __uint_as_float((254u - ms) << 23));
   unsigned mw[PER / 2], vr[PER];
 #pragma unroll
   for (int q = 0; q < PER / 2; ++q)
-    mw[q] = __nv_cvt_float2_to_fp8x2(make_float2(m[2 * q] * mi, m[2 * q + 1] * mi), __NV_SATFINITE, __NV_E4M3);
+    mw[q] = __nv_cvt_float2_to_fp8x2(make_float2(m[2 * q], m[2 * q + 1]), __NV_SATFINITE, __NV_E4M3);
   if (stochastic) second_codes<true>(vr, v, scaled, n);
   else second_codes<false>(vr, v, scaled, n);
-  if (odd != 0) {
+  if (rare(odd != 0)) {
 #pragma unroll
     for (int j = 0; j < PER; ++j)
       if (odd & (1u << j)) vr[j] = 255u << 24;
@@ -489,9 +520,13 @@ __device__ __forceinline__ float reciprocal_fast(float x) {
 }
 
 template <bool TINY>
-__device__ __forceinline__ float new_weight(float w, float m, float v, const Rates& r, float eps) {
-  const float den = fmaf(sqrt_fast<TINY>(v), r.root, eps);
-  return fmaf(r.decay, w, -(r.rate * m) * reciprocal_fast<TINY>(den));
+__device__ __forceinline__ void new_weights(float (&w)[PER], const float (&m)[PER], const float (&v)[PER], const Rates& r,
+                                            float eps) {
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    const float den = fmaf(sqrt_fast<TINY>(v[j]), r.root, eps);
+    w[j] = fmaf(r.decay, w[j], -(r.rate * m[j]) * reciprocal_fast<TINY>(den));
+  }
 }
 
 // m and v come in units of the scales ms and vs, powers of two that the
@@ -504,13 +539,8 @@ __device__ __forceinline__ void update(float (&w)[PER], float (&m)[PER], float (
     m[j] = __fadd_rn(__fmul_rn(b1, m[j]), __fmul_rn(h.c1, g[j]));
     v[j] = __fadd_rn(__fmul_rn(b2, v[j]), __fmul_rn(h.c2, __fmul_rn(g[j], g[j])));
   }
-  if (h.eps >= 1e-10f) {
-#pragma unroll
-    for (int j = 0; j < PER; ++j) w[j] = new_weight<false>(w[j], m[j], v[j], r, h.eps);
-  } else {
-#pragma unroll
-    for (int j = 0; j < PER; ++j) w[j] = new_weight<true>(w[j], m[j], v[j], r, h.eps);
-  }
+  if (rare(h.eps < 1e-10f)) new_weights<true>(w, m, v, r, h.eps);
+  else new_weights<false>(w, m, v, r, h.eps);
 }
 
 // bf16 weights without an fp32 master: to the neighbour above with the
@@ -523,7 +553,7 @@ __device__ __forceinline__ void round_weights(Raw<__nv_bfloat16>& out, const flo
   unsigned u[PER];
 #pragma unroll
   for (int j = 0; j < PER; ++j) u[j] = __float_as_uint(w[j]) + n.bits16(j);
-  if (zero != 0.f) {                                   // the sum may have made a number of a NaN
+  if (rare(zero != 0.f)) {                                   // the sum may have made a number of a NaN
 #pragma unroll
     for (int j = 0; j < PER; ++j)
       if (!(fabsf(w[j]) < __uint_as_float(INF_BITS))) u[j] = __float_as_uint(w[j]);
@@ -547,7 +577,7 @@ struct Shared {
   AwType ct;
   __device__ __forceinline__ void start(const AwHyper& h, const AwTensor& t) {
     r = rates_of(h, t);
-    k = keys_of(h, t.index);
+    if (h.stochastic) k = keys_of(h, t.index);
     ct = t.ct;
   }
 };
@@ -563,19 +593,18 @@ __device__ __forceinline__ void moments_of(float (&m)[PER], float (&v)[PER], con
   const unsigned msb = scales & 0xffu, vsb = scales >> 8;
   ms = scale_of(msb);
   vs = scale_of(vsb);
-  if (min(msb, vsb) < 32) {
+  if (rare(min(msb, vsb) < 32)) {
     // b1 ms or b2 vs may be subnormal and not exact: scale the moments themselves
-#pragma unroll
-    for (int j = 0; j < PER; ++j) {
-      m[j] *= ms;
-      v[j] *= vs;
-    }
+    scale_all(m, ms);
+    scale_all(v, vs);
     ms = vs = 1.f;
   }
 }
 
 template <bool EIGHT, typename WT, typename GT, bool VEC>
 struct StepOp {
+  static constexpr int BATCH = 0;
+  static constexpr bool BACKWARDS = false;
   using Load = StepLoad<EIGHT, WT, GT>;
   using Moment = typename Load::Moment;
   const AwHyper& h;
@@ -620,10 +649,7 @@ struct StepOp {
     float w1[PER], g1[PER], m1[PER], v1[PER];
     widen_all(g1, in.g);
     widen_all(w1, in.w);
-    if (h.gscale != nullptr) {
-#pragma unroll
-      for (int j = 0; j < PER; ++j) g1[j] *= gs;
-    }
+    if (h.gscale != nullptr) scale_all(g1, gs);
     float sm = 1.f, sv = 1.f;
     moments_of(m1, v1, in.m, in.v, sm, sv, EIGHT ? scales.of(r) : 0);
     update(w1, m1, v1, g1, h, s.r, sm, sv);
@@ -676,9 +702,9 @@ __device__ __forceinline__ void StepOp<EIGHT, WT, GT, VEC>::narrow(const AwTenso
   else work_narrow(b, at, r);
 }
 
-template <bool EIGHT, typename WT, typename GT, bool VEC>
-__global__ void __launch_bounds__(AW_THREADS, EIGHT ? STEP8_CTAS : STEP32_CTAS)
-    adamw_kernel(const __grid_constant__ AwTable tab, const __grid_constant__ AwHyper h) {
+template <bool EIGHT, typename WT, typename GT, bool VEC, int N>
+__global__ void __launch_bounds__(AW_THREADS, STEP_CTAS)
+    adamw_kernel(const __grid_constant__ AwTableOf<N> tab, const __grid_constant__ AwHyper h) {
   pdl_wait();
   pdl_trigger();
   if (h.skip != nullptr && *h.skip != 0) return;
@@ -689,6 +715,8 @@ __global__ void __launch_bounds__(AW_THREADS, EIGHT ? STEP8_CTAS : STEP32_CTAS)
 // ---------------------------------------------------------------- pack and unpack
 template <typename T>
 struct PackOp {
+  static constexpr int BATCH = 2;
+  static constexpr bool BACKWARDS = false;
   struct Load {
     Raw<T> m, v;
   };
@@ -709,7 +737,7 @@ struct PackOp {
     v8 = static_cast<Code*>(t.V) + first;
     ms = t.MS + first / AW_BLOCK;
     vs = t.VS + first / AW_BLOCK;
-    k = keys_of(h, t.index);
+    if (h.stochastic) k = keys_of(h, t.index);
     scales.all = 0;
   }
   template <int AT, bool WIDE = true>
@@ -734,8 +762,8 @@ struct PackOp {
   __device__ __forceinline__ void finish(int blocks) const { scales.store(ms, vs, blocks); }
 };
 
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(AW_THREADS) pack_kernel(const __grid_constant__ AwTable tab,
+template <typename T, bool VEC, int N>
+__global__ void __launch_bounds__(AW_THREADS) pack_kernel(const __grid_constant__ AwTableOf<N> tab,
                                                           const __grid_constant__ AwHyper h) {
   pdl_wait();
   pdl_trigger();
@@ -745,6 +773,8 @@ __global__ void __launch_bounds__(AW_THREADS) pack_kernel(const __grid_constant_
 
 template <typename T>
 struct UnpackOp {
+  static constexpr int BATCH = 4;
+  static constexpr bool BACKWARDS = false;
   struct Load {
     Raw<Code> m, v;
   };
@@ -771,11 +801,8 @@ struct UnpackOp {
     decode(x, y, in.m, in.v);
     const unsigned sc = scales.of(r);
     const float sm = scale_of(sc & 0xffu), sv = scale_of(sc >> 8);
-#pragma unroll
-    for (int j = 0; j < PER; ++j) {
-      x[j] *= sm;
-      y[j] *= sv;
-    }
+    scale_all(x, sm);
+    scale_all(y, sv);
     store(x, m + at, b);
     store(y, v + at, b);
   }
@@ -787,8 +814,8 @@ struct UnpackOp {
   __device__ __forceinline__ void finish(int) const {}
 };
 
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(AW_THREADS) unpack_kernel(const __grid_constant__ AwTable tab) {
+template <typename T, bool VEC, int N>
+__global__ void __launch_bounds__(AW_THREADS) unpack_kernel(const __grid_constant__ AwTableOf<N> tab) {
   pdl_wait();
   pdl_trigger();
   UnpackOp<T> op;
@@ -796,12 +823,11 @@ __global__ void __launch_bounds__(AW_THREADS) unpack_kernel(const __grid_constan
 }
 
 // ---------------------------------------------------------------- clipping
-constexpr int FINISH_THREADS = 256;
-
 // norm    sum of squares: 8 at a time in fp32, then fp64; one partial sum per
 //         CTA, in an order that the grid alone fixes
 // finish  the partial sums in a fixed order, the norm and the factor
-// scale   out = factor * G
+// scale   out = factor * G, the last runs first: L2 still holds them.  With few
+//         partial sums every CTA sums them itself and `finish` is left out.
 __device__ __forceinline__ double warp_sum(double x) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
@@ -810,6 +836,8 @@ __device__ __forceinline__ double warp_sum(double x) {
 
 template <typename T>
 struct NormOp {
+  static constexpr int BATCH = 4;
+  static constexpr bool BACKWARDS = false;
   using Load = Raw<T>;
   double sum = 0.0;
   const T* g;
@@ -832,8 +860,8 @@ struct NormOp {
   __device__ __forceinline__ void finish(int) const {}
 };
 
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(AW_THREADS) norm_kernel(const __grid_constant__ AwTable tab, double* partial) {
+template <typename T, bool VEC, int N>
+__global__ void __launch_bounds__(AW_THREADS) norm_kernel(const __grid_constant__ AwTableOf<N> tab, double* partial) {
   pdl_wait();
   pdl_trigger();
   NormOp<T> op;
@@ -842,30 +870,51 @@ __global__ void __launch_bounds__(AW_THREADS) norm_kernel(const __grid_constant_
   if (threadIdx.x == 0) partial[blockIdx.x] = s;
 }
 
+// The factor from the sum of all squares; the caller with `write` stores the results.
+__device__ __forceinline__ float factor_of(const ClipArgs& a, double squares, bool write) {
+  const float scale = a.scale ? *a.scale : 1.f;
+  const float norm = (float)(fabs((double)scale) * sqrt(squares));
+  const float f = a.max_norm / (norm + 1e-6f);
+  // a norm that is not a number gives such a factor (1 only where f >= 1)
+  const float factor = scale * (f >= 1.f ? 1.f : f);
+  if (write) {
+    *a.norm = norm;
+    *a.factor = factor;
+    if (a.nonfinite) *a.nonfinite = isfinite(norm) ? 0 : 1;
+  }
+  return factor;
+}
+
+// The sum of at most FEW_PARTS partial sums, the same in every lane of a warp.
+__device__ __forceinline__ double sum_few(const ClipArgs& a) {
+  double sum = 0.0;
+  for (int i = threadIdx.x % 32; i < a.parts; i += 32) sum += a.partial[i];
+  return warp_sum(sum);
+}
+
 __global__ void __launch_bounds__(FINISH_THREADS) finish_kernel(const __grid_constant__ ClipArgs a) {
   __shared__ double red[FINISH_THREADS / 32];
   pdl_wait();
   pdl_trigger();
-  double sum = 0.0;
-  for (int i = threadIdx.x; i < a.parts; i += FINISH_THREADS) sum += a.partial[i];
-  sum = warp_sum(sum);
-  if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = sum;
-  __syncthreads();
-  if (threadIdx.x != 0) return;
   double s = 0.0;
+  if (a.parts <= FEW_PARTS) {
+    s = sum_few(a);
+  } else {
+    double sum = 0.0;
+    for (int i = threadIdx.x; i < a.parts; i += FINISH_THREADS) sum += a.partial[i];
+    sum = warp_sum(sum);
+    if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = sum;
+    __syncthreads();
 #pragma unroll
-  for (int k = 0; k < FINISH_THREADS / 32; ++k) s += red[k];
-  const float scale = a.scale ? *a.scale : 1.f;
-  const float norm = (float)(fabs((double)scale) * sqrt(s));
-  const float f = a.max_norm / (norm + 1e-6f);
-  // a norm that is not a number gives such a factor (1 only where f >= 1)
-  *a.norm = norm;
-  *a.factor = scale * (f >= 1.f ? 1.f : f);
-  if (a.nonfinite) *a.nonfinite = isfinite(norm) ? 0 : 1;
+    for (int k = 0; k < FINISH_THREADS / 32; ++k) s += red[k];
+  }
+  if (threadIdx.x == 0) factor_of(a, s, true);
 }
 
 template <typename T, typename OUT>
 struct ScaleOp {
+  static constexpr int BATCH = 4;
+  static constexpr bool BACKWARDS = true;
   using Load = Raw<T>;
   float f;
   const T* g;
@@ -880,8 +929,7 @@ struct ScaleOp {
   __device__ __forceinline__ void work(const Load& in, const Place<WIDE>& b, unsigned at, int) const {
     float x[PER];
     widen_all(x, in);
-#pragma unroll
-    for (int j = 0; j < PER; ++j) x[j] *= f;
+    scale_all(x, f);
     store(x, out + at, b);
   }
   __device__ __forceinline__ void narrow(const AwTensor&, const Place<false>& b, unsigned at, int r) const {
@@ -892,27 +940,15 @@ struct ScaleOp {
   __device__ __forceinline__ void finish(int) const {}
 };
 
-template <typename T, typename OUT, bool VEC>
-__global__ void __launch_bounds__(AW_THREADS) scale_kernel(const __grid_constant__ AwTable tab, const float* factor) {
+template <typename T, typename OUT, bool VEC, int N>
+__global__ void __launch_bounds__(AW_THREADS) scale_kernel(const __grid_constant__ AwTableOf<N> tab,
+                                                           const __grid_constant__ ClipArgs a) {
   pdl_wait();
   pdl_trigger();
   ScaleOp<T, OUT> op;
-  op.f = *factor;
+  op.f = a.finish_here ? factor_of(a, sum_few(a), blockIdx.x == 0 && threadIdx.x == 0) : *a.factor;
   walk<VEC>(tab, op);
 }
-
-// CTAs of a launch: as many as fit on the card, at most one per run.
-unsigned grid_of(const AwTable& t, int per_sm) {
-  const unsigned most = (unsigned)(device_sm_count() * per_sm);
-  return t.runs < most ? t.runs : most;
-}
-
-#ifndef PACK_CTAS
-#define PACK_CTAS 24
-#endif
-#ifndef CPL
-#define CPL 32
-#endif
 
 // Calls f with a null pointer of the element type t.
 template <typename F>
@@ -928,12 +964,28 @@ cudaError_t with_wide_type(AwType t, F f) {
 template <typename P>
 using Pointee = typename std::remove_pointer<P>::type;
 
-template <typename... KArgs, typename... Args>
-cudaError_t launch_list(void (*kern)(AwTable, KArgs...), int kind, const AwTable& t, unsigned grid, cudaStream_t s,
-                        Args&&... args) {
+// Launches one of four forms of a kernel: for aligned tensors or others, with a
+// short or a full table (its first AW_SHORT tensors are all that the short form
+// reads; 26 KB of parameters cost a launch 1.1 us more than 6).  The further
+// argument is passed by its address, like the table, and copied once.
+template <typename Arg>
+cudaError_t launch_list(const void* (&forms)[2][2], int kind, const AwTable& t, unsigned grid, const Arg& arg, cudaStream_t s) {
   ProfScope prof(kind, s);
-  return launch_pdl(kern, dim3(grid), dim3(AW_THREADS), 0, s, false, t, std::forward<Args>(args)...);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(AW_THREADS);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl_off() ? 0 : 1;
+  void* args[] = {const_cast<AwTable*>(&t), const_cast<Arg*>(&arg)};
+  return cudaLaunchKernelExC(&cfg, forms[t.t[0].vec != 0][t.n > AW_SHORT], args);
 }
+#define MO_FORMS(KERNEL, ...)                                                                                       \
+  {{(const void*)KERNEL<__VA_ARGS__, false, AW_SHORT>, (const void*)KERNEL<__VA_ARGS__, false, AW_MAX>},            \
+   {(const void*)KERNEL<__VA_ARGS__, true, AW_SHORT>, (const void*)KERNEL<__VA_ARGS__, true, AW_MAX>}}
 
 template <bool EIGHT>
 cudaError_t launch_step(const AwTable& t, const AwHyper& h, cudaStream_t s) {
@@ -941,23 +993,26 @@ cudaError_t launch_step(const AwTable& t, const AwHyper& h, cudaStream_t s) {
     return with_type(t.t[0].gt, [&](auto* g) {
       using W = Pointee<decltype(w)>;
       using G = Pointee<decltype(g)>;
-      return launch_list(t.t[0].vec ? adamw_kernel<EIGHT, W, G, true> : adamw_kernel<EIGHT, W, G, false>, PK_ADAMW, t,
-                         grid_of(t, EIGHT ? STEP8_CTAS : STEP32_CTAS), s, h);
+      const void* forms[2][2] = MO_FORMS(adamw_kernel, EIGHT, W, G);
+      return launch_list(forms, PK_ADAMW, t, t.runs, h, s);
     });
   });
 }
 
 }  // namespace
 
-int run_of(long long blocks) {
-#ifdef RUN
-  return RUN;
-#else
-  const long long warps = (long long)device_sm_count() * STEP8_CTAS;
+// A CTA for each run: the hardware hands runs out as CTAs end, which balances
+// better than a fixed share for each of as many CTAs as fit (218 M elements:
+// fp32 step 1000 -> 905 us, 8-bit step 473 -> 454).  Long runs share the search
+// for their tensor, its rates and, with 8 bits, the sectors of the scales;
+// short ones spread a short list over the card.  65 tensors of 4096 (1040
+// blocks): 3.3 us with runs of 1, 7.7 with 8; 218 M elements, 8 bits and
+// unpacking: 1759 us with runs of 1, 685 with 4, 621 with 8; fp32: 906 with
+// 1, 903 with 2, 951 with 8.
+int run_of(long long blocks, int most) {
   int run = 1;
-  while (run < AW_RUN && blocks >= 8 * run * warps) run *= 2;
+  while (run < most && blocks >= 16ll * run * device_sm_count()) run *= 2;
   return run;
-#endif
 }
 
 cudaError_t launch_adamw(const AwTable& t, const AwHyper& h, cudaStream_t s) { return launch_step<false>(t, h, s); }
@@ -965,44 +1020,39 @@ cudaError_t launch_adamw8(const AwTable& t, const AwHyper& h, cudaStream_t s) { 
 
 cudaError_t launch_pack(const AwTable& t, const AwHyper& h, cudaStream_t s) {
   return with_wide_type(t.t[0].gt, [&](auto* m) {
-    using T = Pointee<decltype(m)>;
-    return launch_list(t.t[0].vec ? pack_kernel<T, true> : pack_kernel<T, false>, PK_MOMENTS, t,
-                       grid_of(t, PACK_CTAS), s, h);
+    const void* forms[2][2] = MO_FORMS(pack_kernel, Pointee<decltype(m)>);
+    return launch_list(forms, PK_MOMENTS, t, t.runs, h, s);
   });
 }
 
 cudaError_t launch_unpack(const AwTable& t, cudaStream_t s) {
   return with_wide_type(t.t[0].wt, [&](auto* m) {
-    using T = Pointee<decltype(m)>;
-    return launch_list(t.t[0].vec ? unpack_kernel<T, true> : unpack_kernel<T, false>, PK_MOMENTS, t,
-                       grid_of(t, CPL), s);
+    const void* forms[2][2] = MO_FORMS(unpack_kernel, Pointee<decltype(m)>);
+    return launch_list(forms, PK_MOMENTS, t, t.runs, 0, s);
   });
 }
 
-int clip_norm_ctas(const AwTable& t, int most) {
-  const unsigned g = grid_of(t, CPL);
-  return (int)(g < (unsigned)most ? g : (unsigned)most);
-}
+int clip_norm_ctas(const AwTable& t, int most) { return t.runs < (unsigned)most ? (int)t.runs : most; }
 
 cudaError_t launch_clip_norm(const AwTable& t, double* partial, int ctas, cudaStream_t s) {
   return with_type(t.t[0].gt, [&](auto* g) {
-    using G = Pointee<decltype(g)>;
-    return launch_list(t.t[0].vec ? norm_kernel<G, true> : norm_kernel<G, false>, PK_CLIP, t, ctas, s, partial);
+    const void* forms[2][2] = MO_FORMS(norm_kernel, Pointee<decltype(g)>);
+    return launch_list(forms, PK_CLIP, t, (unsigned)ctas, partial, s);
   });
 }
 
 cudaError_t launch_clip_finish(const ClipArgs& a, cudaStream_t s) {
   ProfScope prof(PK_CLIP, s);
-  return launch_pdl(finish_kernel, dim3(1), dim3(FINISH_THREADS), 0, s, false, a);
+  return launch_pdl(finish_kernel, dim3(1), dim3(a.parts <= FEW_PARTS ? 32 : FINISH_THREADS), 0, s, false, a);
 }
 
-cudaError_t launch_clip_scale(const AwTable& t, const float* factor, cudaStream_t s) {
+cudaError_t launch_clip_scale(const AwTable& t, const ClipArgs& a, cudaStream_t s) {
   return with_type(t.t[0].gt, [&](auto* g) {
     return with_type(t.t[0].ct, [&](auto* o) {
       using G = Pointee<decltype(g)>;
       using O = Pointee<decltype(o)>;
-      return launch_list(t.t[0].vec ? scale_kernel<G, O, true> : scale_kernel<G, O, false>, PK_CLIP, t,
-                         grid_of(t, CPL), s, factor);
+      const void* forms[2][2] = MO_FORMS(scale_kernel, G, O);
+      return launch_list(forms, PK_CLIP, t, t.runs, a, s);
     });
   });
 }

@@ -11,8 +11,10 @@ namespace mo {
 
 constexpr int AW_BLOCK = 256;      // elements that share a scale of the 8-bit moments
 constexpr int AW_THREADS = 32;     // a CTA is one warp, which works on one block at a time
-constexpr int AW_RUN = 32;         // most blocks of a run: their scales are one 32-byte sector
-constexpr int AW_MAX = 320;        // tensors per launch (the table travels in the kernel's parameters)
+constexpr int AW_RUN = 8;          // most blocks of a run (fp32 moments: AW_RUN32)
+constexpr int AW_RUN32 = 2;
+constexpr int AW_MAX = 350;        // tensors per launch (the table travels in the kernel's parameters)
+constexpr int AW_SHORT = 64;       // tensors that a launch with fewer parameters takes
 
 enum AwType : unsigned char { AW_F32 = 0, AW_BF16 = 1, AW_F16 = 2, AW_NONE = 3 };
 
@@ -34,17 +36,19 @@ struct AwTensor {
   long long numel;
   float lr_scale, wd;
   unsigned index;                  // place in the caller's list (noise stream)
+  unsigned first;                  // its first run among those of the table
   AwType wt, gt, ct;
   unsigned char vec;               // every pointer aligned for the wide path
 };
 
-struct AwTable {
+template <int N>
+struct AwTableOf {
   int n;
   int run;                         // blocks of a run, the work that a CTA takes at a time
-  unsigned runs;                   // first[n]
-  unsigned first[AW_MAX + 1];      // first run of each tensor
-  AwTensor t[AW_MAX];
+  unsigned runs;
+  AwTensor t[N];
 };
+using AwTable = AwTableOf<AW_MAX>;
 
 struct AwHyper {
   float b1, c1, b2, c2;            // beta, 1 - beta
@@ -63,6 +67,7 @@ struct AwHyper {
 struct ClipArgs {
   double* partial;                 // one sum of squares per CTA
   int parts;                       // number of partial sums
+  int finish_here;                 // the scale launch sums them itself
   float max_norm;
   const float* scale;              // optional factor of the gradients
   float* norm;
@@ -71,9 +76,11 @@ struct ClipArgs {
 };
 
 constexpr int CLIP_MAX_CTAS = 8192;   // partial sums of one call
+constexpr int FEW_PARTS = 256;        // partial sums that one warp takes
+constexpr int FINISH_THREADS = 256;
 
-// Blocks of a run (at most AW_RUN) for a list of so many blocks.
-int run_of(long long blocks);
+// Blocks of a run, at most `most`, for a list of so many blocks.
+int run_of(long long blocks, int most);
 cudaError_t launch_adamw(const AwTable& t, const AwHyper& h, cudaStream_t s);
 cudaError_t launch_adamw8(const AwTable& t, const AwHyper& h, cudaStream_t s);
 cudaError_t launch_pack(const AwTable& t, const AwHyper& h, cudaStream_t s);
@@ -82,6 +89,6 @@ cudaError_t launch_unpack(const AwTable& t, cudaStream_t s);
 int clip_norm_ctas(const AwTable& t, int most);
 cudaError_t launch_clip_norm(const AwTable& t, double* partial, int ctas, cudaStream_t s);
 cudaError_t launch_clip_finish(const ClipArgs& a, cudaStream_t s);
-cudaError_t launch_clip_scale(const AwTable& t, const float* factor, cudaStream_t s);
+cudaError_t launch_clip_scale(const AwTable& t, const ClipArgs& a, cudaStream_t s);
 
 }  // namespace mo

@@ -3,6 +3,7 @@
 #include <algorithm>
 #include <cmath>
 #include <exception>
+#include <memory>
 #include <string>
 #include <vector>
 
@@ -74,43 +75,49 @@ bool numel_ok(int64_t numel, int i) {
 
 size_t blocks_of(int64_t numel) { return (size_t)((numel + AW_BLOCK - 1) / AW_BLOCK); }
 
-// Splits the list into launches of one set of types, of aligned tensors or of
-// others, and of at most AW_MAX tensors.
+// The tables of a list: launches of one set of types, of aligned tensors or of
+// others, and of at most AW_MAX tensors each.
 class Tables {
  public:
-  explicit Tables(bool by_output = false) : by_output_(by_output) { std::fill_n(&open_[0][0][0], 2 * 4 * 4, -1); }
+  // most_run: the longest run; by_output: clip_grads leaves wt alone and
+  // launches by the output's type instead
+  explicit Tables(int most_run, bool by_output = false) : most_run_(most_run), by_output_(by_output) {
+    std::fill_n(&open_[0][0][0], 2 * 4 * 4, -1);
+  }
   void add(const AwTensor& t) {
-    // clip_grads leaves wt alone and launches by the output's type instead
     int& open = open_[t.vec][by_output_ ? t.ct : t.wt][t.gt];
     const long long blocks = (long long)blocks_of(t.numel);
-    if (open < 0 || tabs_[open].n == AW_MAX || blocks_[open] + blocks > MAX_BLOCKS) {
+    if (open < 0 || tabs_[open]->n == AW_MAX || blocks_[open] + blocks > MAX_BLOCKS) {
       open = (int)tabs_.size();
-      tabs_.emplace_back();
-      tabs_.back().n = 0;
+      tabs_.emplace_back(new AwTable);
+      tabs_.back()->n = 0;
       blocks_.push_back(0);
     }
-    tabs_[open].t[tabs_[open].n++] = t;
+    tabs_[open]->t[tabs_[open]->n++] = t;
     blocks_[open] += blocks;
   }
   // Divides the tensors into runs, once all are in.
   void finish() {
     for (size_t k = 0; k < tabs_.size(); ++k) {
-      AwTable& tab = tabs_[k];
-      tab.run = run_of(blocks_[k]);
-      tab.first[0] = 0;
-      for (int i = 0; i < tab.n; ++i)
-        tab.first[i + 1] = tab.first[i] + (unsigned)((blocks_of(tab.t[i].numel) + tab.run - 1) / tab.run);
-      tab.runs = tab.first[tab.n];
+      AwTable& tab = *tabs_[k];
+      tab.run = run_of(blocks_[k], most_run_);
+      tab.runs = 0;
+      for (int i = 0; i < tab.n; ++i) {
+        tab.t[i].first = tab.runs;
+        tab.runs += (unsigned)((blocks_of(tab.t[i].numel) + tab.run - 1) / tab.run);
+      }
     }
   }
-  const std::vector<AwTable>& all() const { return tabs_; }
+  size_t size() const { return tabs_.size(); }
+  const AwTable& operator[](size_t k) const { return *tabs_[k]; }
 
  private:
   static constexpr long long MAX_BLOCKS = 0x7fffffffll;
-  std::vector<AwTable> tabs_;
+  int most_run_;
+  bool by_output_;
+  std::vector<std::unique_ptr<AwTable>> tabs_;
   std::vector<long long> blocks_;
   int open_[2][4][4];              // the table that takes the next such tensor
-  bool by_output_;
 };
 
 bool finite_nonneg(double x) { return std::isfinite(x) && x >= 0.0; }
@@ -178,11 +185,11 @@ AwTensor step_tensor(const T& a, int i, std::vector<Range>& r) {
 }
 
 template <typename T>
-void codes(const T& a, int i, std::vector<Range>& r, bool written, AwTensor& t) {
-  buffer(r, a.M8, a.numel, 1, written, "M8", i);
-  buffer(r, a.V8, a.numel, 1, written, "V8", i);
-  buffer(r, a.MS, (int64_t)blocks_of(a.numel), 1, written, "MS", i);
-  buffer(r, a.VS, (int64_t)blocks_of(a.numel), 1, written, "VS", i);
+void codes(const T& a, int i, std::vector<Range>& r, AwTensor& t) {
+  buffer(r, a.M8, a.numel, 1, true, "M8", i);
+  buffer(r, a.V8, a.numel, 1, true, "V8", i);
+  buffer(r, a.MS, (int64_t)blocks_of(a.numel), 1, true, "MS", i);
+  buffer(r, a.VS, (int64_t)blocks_of(a.numel), 1, true, "VS", i);
   t.M = a.M8;
   t.V = a.V8;
   t.MS = a.MS;
@@ -193,17 +200,10 @@ void codes(const T& a, int i, std::vector<Range>& r, bool written, AwTensor& t) 
 }
 
 // Runs the body of an entry point: nothing is thrown across the C boundary.
-// The body validates first, then calls launch() with what it launches, which
-// runs with the context's device current.
 template <typename F>
 mo_status guarded(mo_ctx* ctx, const char* who, F body) {
   try {
-    const auto launch = [ctx](auto launches) {
-      DeviceScope scope;
-      const cudaError_t e = scope.enter(ctx_device(ctx));
-      return e == cudaSuccess ? launches() : e;
-    };
-    const cudaError_t e = body(launch);
+    const cudaError_t e = body();
     if (e != cudaSuccess) return ctx_fail(ctx, MO_ERR_CUDA, std::string(who) + ": " + cudaGetErrorString(e));
     return MO_OK;
   } catch (const Refused& r) {
@@ -213,18 +213,224 @@ mo_status guarded(mo_ctx* ctx, const char* who, F body) {
   }
 }
 
-mo_status check_list(mo_ctx* ctx, const char* who, const void* list, int n, const void* cfg) {
-  if (ctx == nullptr) return MO_ERR_INVALID_ARG;
-  if (n < 0) return ctx_fail(ctx, MO_ERR_INVALID_ARG, std::string(who) + ": n < 0");
-  if (n > 0 && (list == nullptr || cfg == nullptr))
-    return ctx_fail(ctx, MO_ERR_INVALID_ARG, std::string(who) + ": null list or cfg");
-  return MO_OK;
+// launches() with the context's device current.
+template <typename F>
+cudaError_t on_device(mo_ctx* ctx, F launches) {
+  DeviceScope scope;
+  const cudaError_t e = scope.enter(ctx_device(ctx));
+  return e == cudaSuccess ? launches() : e;
+}
+
+template <typename F>
+cudaError_t launch_all(mo_ctx* ctx, const Tables& tabs, F launch) {
+  return on_device(ctx, [&]() {
+    cudaError_t e = cudaSuccess;
+    for (size_t k = 0; k < tabs.size() && e == cudaSuccess; ++k) e = launch(tabs[k]);
+    return e;
+  });
 }
 
 struct ProfBind {
   explicit ProfBind(mo_ctx* c) { g_prof = c ? ctx_profiler(c) : nullptr; }
   ~ProfBind() { g_prof = nullptr; }
 };
+
+enum ListKind { LIST_ADAMW, LIST_ADAMW8, LIST_MOMENTS, LIST_GRADS };
+
+}  // namespace
+
+}  // namespace mo
+
+// A checked list with its launch tables.
+struct mo_list {
+  mo::ListKind kind;
+  mo::Tables tabs;
+  std::vector<mo::Range> ranges;       // sorted
+};
+
+namespace mo {
+
+namespace {
+
+// Whether [p, p + bytes) meets a range of the list.
+bool touches(const mo_list& l, const void* p, size_t bytes) {
+  const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+  for (const Range& x : l.ranges)
+    if (p != nullptr && lo < x.hi && x.lo < lo + bytes) return true;
+  return false;
+}
+
+template <typename T, typename F>
+std::unique_ptr<mo_list> build(ListKind kind, const T* list, int n, Tables tabs, F fill) {
+  if (n < 0) refuse("n < 0");
+  if (n > 0 && list == nullptr) refuse("null list");
+  std::unique_ptr<mo_list> l(new mo_list{kind, std::move(tabs), {}});
+  l->ranges.reserve((size_t)n * 7);
+  for (int i = 0; i < n; ++i)
+    if (numel_ok(list[i].numel, i)) fill(list[i], i, *l);
+  check_apart(l->ranges);
+  l->tabs.finish();
+  return l;
+}
+
+std::unique_ptr<mo_list> build_adamw(const mo_adamw_tensor* list, int n) {
+  return build(LIST_ADAMW, list, n, Tables(AW_RUN32), [](const mo_adamw_tensor& a, int i, mo_list& l) {
+    if (a.G == nullptr) return;
+    AwTensor t = step_tensor(a, i, l.ranges);
+    buffer(l.ranges, a.M, a.numel, 4, true, "M", i);
+    buffer(l.ranges, a.V, a.numel, 4, true, "V", i);
+    t.M = a.M;
+    t.V = a.V;
+    t.vec = t.vec && aligned(a.M, 32) && aligned(a.V, 32);
+    l.tabs.add(t);
+  });
+}
+
+std::unique_ptr<mo_list> build_adamw8(const mo_adamw8_tensor* list, int n) {
+  return build(LIST_ADAMW8, list, n, Tables(AW_RUN), [](const mo_adamw8_tensor& a, int i, mo_list& l) {
+    if (a.G == nullptr) return;
+    AwTensor t = step_tensor(a, i, l.ranges);
+    codes(a, i, l.ranges, t);
+    l.tabs.add(t);
+  });
+}
+
+// One table serves both directions: pack reads M and V through G and C, unpack
+// writes them through W and C.
+std::unique_ptr<mo_list> build_moments(const mo_adamw8_moments* list, int n) {
+  return build(LIST_MOMENTS, list, n, Tables(AW_RUN), [](const mo_adamw8_moments& a, int i, mo_list& l) {
+    if (a.type != MO_F32 && a.type != MO_BF16) refuse("type must be MO_F32 or MO_BF16" + at(i));
+    AwTensor t = {};
+    t.wt = t.gt = (AwType)a.type;
+    buffer(l.ranges, a.M, a.numel, width(a.type), true, "M", i);
+    buffer(l.ranges, a.V, a.numel, width(a.type), true, "V", i);
+    t.W = a.M;
+    t.G = a.M;
+    t.C = a.V;
+    t.vec = aligned(a.M, 8 * width(a.type)) && aligned(a.V, 8 * width(a.type));
+    codes(a, i, l.ranges, t);
+    l.tabs.add(t);
+  });
+}
+
+std::unique_ptr<mo_list> build_grads(const mo_grad* list, int n) {
+  return build(LIST_GRADS, list, n, Tables(AW_RUN, true), [](const mo_grad& a, int i, mo_list& l) {
+    if (a.G == nullptr) return;
+    const bool in_place = a.out == nullptr || a.out == a.G;
+    if (!type_ok(a.g_type) || (a.out != nullptr && !type_ok(a.out_type))) refuse("bad g_type or out_type" + at(i));
+    if (in_place && a.out != nullptr && a.out_type != a.g_type) refuse("out in place must keep G's type" + at(i));
+    AwTensor t = {};
+    t.gt = (AwType)a.g_type;
+    t.ct = in_place ? t.gt : (AwType)a.out_type;
+    buffer(l.ranges, a.G, a.numel, width(t.gt), in_place, "G", i);
+    if (!in_place) buffer(l.ranges, a.out, a.numel, width(t.ct), true, "out", i);
+    t.G = a.G;
+    t.C = in_place ? const_cast<void*>(a.G) : a.out;
+    t.vec = aligned(a.G, 8 * width(t.gt)) && aligned(t.C, 8 * width(t.ct));
+    t.numel = a.numel;
+    t.index = (unsigned)i;
+    l.tabs.add(t);
+  });
+}
+
+const mo_list& of_kind(const mo_list* l, ListKind kind) {
+  if (l == nullptr) refuse("null list");
+  if (l->kind != kind) refuse("a list made for another call");
+  return *l;
+}
+
+template <typename T>
+const T& given(const T* cfg) {
+  if (cfg == nullptr) refuse("null cfg");
+  return *cfg;
+}
+
+cudaError_t run_adamw(mo_ctx* ctx, const mo_list& l, const mo_adamw_cfg& cfg, int64_t step, void* stream) {
+  const AwHyper h = hyper(cfg, step);
+  const bool eight = l.kind == LIST_ADAMW8;
+  return launch_all(ctx, l.tabs, [&](const AwTable& tab) {
+    return eight ? launch_adamw8(tab, h, static_cast<cudaStream_t>(stream))
+                 : launch_adamw(tab, h, static_cast<cudaStream_t>(stream));
+  });
+}
+
+cudaError_t run_pack(mo_ctx* ctx, const mo_list& l, const mo_pack_cfg& cfg, void* stream) {
+  AwHyper h = {};
+  if (!aligned(cfg.step_dev, 8)) refuse("device scalars must be aligned to their type");
+  h.stochastic = cfg.stochastic != 0;
+  h.seed = cfg.seed;
+  h.step = cfg.step;
+  h.step_dev = reinterpret_cast<const long long*>(cfg.step_dev);
+  return launch_all(ctx, l.tabs,
+                    [&](const AwTable& tab) { return launch_pack(tab, h, static_cast<cudaStream_t>(stream)); });
+}
+
+cudaError_t run_unpack(mo_ctx* ctx, const mo_list& l, void* stream) {
+  return launch_all(ctx, l.tabs,
+                    [&](const AwTable& tab) { return launch_unpack(tab, static_cast<cudaStream_t>(stream)); });
+}
+
+cudaError_t run_clip(mo_ctx* ctx, const mo_list& l, const mo_clip_cfg& cfg, void* stream) {
+  if (!(cfg.max_norm >= 0.f)) refuse("max_norm must be >= 0");
+  if (cfg.norm == nullptr || cfg.factor == nullptr) refuse("null norm or factor");
+  const void* scalars[] = {cfg.norm, cfg.factor, cfg.nonfinite, cfg.scale};   // the last is read
+  std::vector<Range> r;
+  for (int k = 0; k < 4; ++k) {
+    if (!aligned(scalars[k], 4)) refuse("device scalars must be aligned to their type");
+    if (touches(l, scalars[k], 4)) refuse("buffers overlap");
+    add(r, scalars[k], 4, k < 3);
+  }
+  check_apart(r);
+  size_t ws_bytes = 0;
+  char* ws = ctx_workspace(ctx, &ws_bytes);
+  if (ws == nullptr || ws_bytes < MO_CLIP_WORKSPACE_BYTES)
+    refuse("needs an attached workspace of MO_CLIP_WORKSPACE_BYTES", MO_ERR_NO_WORKSPACE);
+  ClipArgs a = {};
+  a.partial = reinterpret_cast<double*>(ws + WS_HEADER);
+  a.max_norm = cfg.max_norm;
+  a.scale = cfg.scale;
+  a.norm = cfg.norm;
+  a.factor = cfg.factor;
+  a.nonfinite = cfg.nonfinite;
+  // several tables share the fixed number of partial sums
+  const int each = l.tabs.size() == 0 ? 0 : CLIP_MAX_CTAS / (int)l.tabs.size();
+  if (l.tabs.size() > 0 && each == 0) refuse("too many tensors");
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return on_device(ctx, [&]() {
+    cudaError_t e = cudaSuccess;
+    for (size_t k = 0; k < l.tabs.size() && e == cudaSuccess; ++k) {
+      const int ctas = clip_norm_ctas(l.tabs[k], each);
+      e = launch_clip_norm(l.tabs[k], a.partial + a.parts, ctas, s);
+      a.parts += ctas;
+    }
+    // with one table and few sums its scale launch finishes them
+    a.finish_here = cfg.apply && l.tabs.size() == 1 && a.parts <= FEW_PARTS;
+    if (!a.finish_here && e == cudaSuccess) e = launch_clip_finish(a, s);
+    for (size_t k = 0; k < l.tabs.size() && e == cudaSuccess && cfg.apply; ++k) e = launch_clip_scale(l.tabs[k], a, s);
+    return e;
+  });
+}
+
+// Makes a list of `kind` for the caller.
+template <typename F>
+mo_status make_list(mo_ctx* ctx, const char* who, mo_list** out, F build_it) {
+  if (ctx == nullptr) return MO_ERR_INVALID_ARG;
+  return guarded(ctx, who, [&]() {
+    if (out == nullptr) refuse("null out");
+    *out = nullptr;
+    *out = build_it().release();
+    return cudaSuccess;
+  });
+}
+
+// An entry point that runs: profiler, range for timeline tools, errors.
+template <typename F>
+mo_status entry(mo_ctx* ctx, const char* who, const char* range, F body) {
+  if (ctx == nullptr) return MO_ERR_INVALID_ARG;
+  ProfBind prof(ctx);
+  NvtxRange nvtx(range);
+  return guarded(ctx, who, body);
+}
 
 }  // namespace
 
@@ -234,221 +440,70 @@ using namespace mo;
 
 extern "C" {
 
+mo_status mo_adamw_list(mo_ctx* ctx, const mo_adamw_tensor* list, int n, mo_list** out) {
+  return make_list(ctx, "adamw_step", out, [&]() { return build_adamw(list, n); });
+}
+mo_status mo_adamw8_list(mo_ctx* ctx, const mo_adamw8_tensor* list, int n, mo_list** out) {
+  return make_list(ctx, "adamw8_step", out, [&]() { return build_adamw8(list, n); });
+}
+mo_status mo_moments_list(mo_ctx* ctx, const mo_adamw8_moments* list, int n, mo_list** out) {
+  return make_list(ctx, "adamw8_moments", out, [&]() { return build_moments(list, n); });
+}
+mo_status mo_grad_list(mo_ctx* ctx, const mo_grad* list, int n, mo_list** out) {
+  return make_list(ctx, "clip_grads", out, [&]() { return build_grads(list, n); });
+}
+void mo_list_destroy(mo_list* list) { delete list; }
+
+mo_status adamw_step_list(mo_ctx* ctx, const mo_list* list, const mo_adamw_cfg* cfg, int64_t step, void* stream) {
+  return entry(ctx, "adamw_step", "mo adamw_step",
+               [&]() { return run_adamw(ctx, of_kind(list, LIST_ADAMW), given(cfg), step, stream); });
+}
+mo_status adamw8_step_list(mo_ctx* ctx, const mo_list* list, const mo_adamw_cfg* cfg, int64_t step, void* stream) {
+  return entry(ctx, "adamw8_step", "mo adamw8_step",
+               [&]() { return run_adamw(ctx, of_kind(list, LIST_ADAMW8), given(cfg), step, stream); });
+}
+mo_status adamw8_pack_list(mo_ctx* ctx, const mo_list* list, const mo_pack_cfg* cfg, void* stream) {
+  return entry(ctx, "adamw8_pack", "mo adamw8_pack",
+               [&]() { return run_pack(ctx, of_kind(list, LIST_MOMENTS), given(cfg), stream); });
+}
+mo_status adamw8_unpack_list(mo_ctx* ctx, const mo_list* list, void* stream) {
+  return entry(ctx, "adamw8_unpack", "mo adamw8_unpack",
+               [&]() { return run_unpack(ctx, of_kind(list, LIST_MOMENTS), stream); });
+}
+mo_status clip_grads_list(mo_ctx* ctx, const mo_list* list, const mo_clip_cfg* cfg, void* stream) {
+  return entry(ctx, "clip_grads", "mo clip_grads",
+               [&]() { return run_clip(ctx, of_kind(list, LIST_GRADS), given(cfg), stream); });
+}
+
 mo_status adamw_step(mo_ctx* ctx, const mo_adamw_tensor* list, int n, const mo_adamw_cfg* cfg, int64_t step,
                      void* stream) {
-  const char* who = "adamw_step";
-  mo_status st = check_list(ctx, who, list, n, cfg);
-  if (st != MO_OK || n == 0) return st;
-  ProfBind prof(ctx);
-  NvtxRange nvtx("mo adamw_step");
-  return guarded(ctx, who, [&](auto launch) {
-    const AwHyper h = hyper(*cfg, step);
-    std::vector<Range> r;
-    r.reserve((size_t)n * 5);
-    Tables tabs;
-    for (int i = 0; i < n; ++i) {
-      const mo_adamw_tensor& a = list[i];
-      if (!numel_ok(a.numel, i) || a.G == nullptr) continue;
-      AwTensor t = step_tensor(a, i, r);
-      buffer(r, a.M, a.numel, 4, true, "M", i);
-      buffer(r, a.V, a.numel, 4, true, "V", i);
-      t.M = a.M;
-      t.V = a.V;
-      t.vec = t.vec && aligned(a.M, 32) && aligned(a.V, 32);
-      tabs.add(t);
-    }
-    check_apart(r);
-    tabs.finish();
-    return launch([&]() {
-      cudaError_t e = cudaSuccess;
-      for (const AwTable& tab : tabs.all())
-        if (e == cudaSuccess) e = launch_adamw(tab, h, static_cast<cudaStream_t>(stream));
-      return e;
-    });
+  return entry(ctx, "adamw_step", "mo adamw_step", [&]() {
+    if (n == 0) return cudaSuccess;
+    return run_adamw(ctx, *build_adamw(list, n), given(cfg), step, stream);
   });
 }
-
 mo_status adamw8_step(mo_ctx* ctx, const mo_adamw8_tensor* list, int n, const mo_adamw_cfg* cfg, int64_t step,
                       void* stream) {
-  const char* who = "adamw8_step";
-  mo_status st = check_list(ctx, who, list, n, cfg);
-  if (st != MO_OK || n == 0) return st;
-  ProfBind prof(ctx);
-  NvtxRange nvtx("mo adamw8_step");
-  return guarded(ctx, who, [&](auto launch) {
-    const AwHyper h = hyper(*cfg, step);
-    std::vector<Range> r;
-    r.reserve((size_t)n * 7);
-    Tables tabs;
-    for (int i = 0; i < n; ++i) {
-      const mo_adamw8_tensor& a = list[i];
-      if (!numel_ok(a.numel, i) || a.G == nullptr) continue;
-      AwTensor t = step_tensor(a, i, r);
-      codes(a, i, r, true, t);
-      tabs.add(t);
-    }
-    check_apart(r);
-    tabs.finish();
-    return launch([&]() {
-      cudaError_t e = cudaSuccess;
-      for (const AwTable& tab : tabs.all())
-        if (e == cudaSuccess) e = launch_adamw8(tab, h, static_cast<cudaStream_t>(stream));
-      return e;
-    });
+  return entry(ctx, "adamw8_step", "mo adamw8_step", [&]() {
+    if (n == 0) return cudaSuccess;
+    return run_adamw(ctx, *build_adamw8(list, n), given(cfg), step, stream);
   });
 }
-
 mo_status adamw8_pack(mo_ctx* ctx, const mo_adamw8_moments* list, int n, const mo_pack_cfg* cfg, void* stream) {
-  const char* who = "adamw8_pack";
-  mo_status st = check_list(ctx, who, list, n, cfg);
-  if (st != MO_OK || n == 0) return st;
-  ProfBind prof(ctx);
-  NvtxRange nvtx("mo adamw8_pack");
-  return guarded(ctx, who, [&](auto launch) {
-    AwHyper h = {};
-    if (!aligned(cfg->step_dev, 8)) refuse("device scalars must be aligned to their type");
-    h.stochastic = cfg->stochastic != 0;
-    h.seed = cfg->seed;
-    h.step = cfg->step;
-    h.step_dev = reinterpret_cast<const long long*>(cfg->step_dev);
-    std::vector<Range> r;
-    r.reserve((size_t)n * 6);
-    Tables tabs;
-    for (int i = 0; i < n; ++i) {
-      const mo_adamw8_moments& a = list[i];
-      if (!numel_ok(a.numel, i)) continue;
-      if (a.type != MO_F32 && a.type != MO_BF16) refuse("type must be MO_F32 or MO_BF16" + at(i));
-      AwTensor t = {};
-      t.gt = (AwType)a.type;
-      buffer(r, a.M, a.numel, width(a.type), false, "M", i);
-      buffer(r, a.V, a.numel, width(a.type), false, "V", i);
-      t.G = a.M;
-      t.C = a.V;
-      t.vec = aligned(a.M, 8 * width(a.type)) && aligned(a.V, 8 * width(a.type));
-      codes(a, i, r, true, t);
-      tabs.add(t);
-    }
-    check_apart(r);
-    tabs.finish();
-    return launch([&]() {
-      cudaError_t e = cudaSuccess;
-      for (const AwTable& tab : tabs.all())
-        if (e == cudaSuccess) e = launch_pack(tab, h, static_cast<cudaStream_t>(stream));
-      return e;
-    });
+  return entry(ctx, "adamw8_pack", "mo adamw8_pack", [&]() {
+    if (n == 0) return cudaSuccess;
+    return run_pack(ctx, *build_moments(list, n), given(cfg), stream);
   });
 }
-
 mo_status adamw8_unpack(mo_ctx* ctx, const mo_adamw8_moments* list, int n, void* stream) {
-  const char* who = "adamw8_unpack";
-  mo_status st = check_list(ctx, who, list, n, list);
-  if (st != MO_OK || n == 0) return st;
-  ProfBind prof(ctx);
-  NvtxRange nvtx("mo adamw8_unpack");
-  return guarded(ctx, who, [&](auto launch) {
-    std::vector<Range> r;
-    r.reserve((size_t)n * 6);
-    Tables tabs;
-    for (int i = 0; i < n; ++i) {
-      const mo_adamw8_moments& a = list[i];
-      if (!numel_ok(a.numel, i)) continue;
-      if (a.type != MO_F32 && a.type != MO_BF16) refuse("type must be MO_F32 or MO_BF16" + at(i));
-      AwTensor t = {};
-      t.wt = (AwType)a.type;
-      buffer(r, a.M, a.numel, width(a.type), true, "M", i);
-      buffer(r, a.V, a.numel, width(a.type), true, "V", i);
-      t.W = a.M;
-      t.C = a.V;
-      t.vec = aligned(a.M, 8 * width(a.type)) && aligned(a.V, 8 * width(a.type));
-      codes(a, i, r, false, t);
-      tabs.add(t);
-    }
-    check_apart(r);
-    tabs.finish();
-    return launch([&]() {
-      cudaError_t e = cudaSuccess;
-      for (const AwTable& tab : tabs.all())
-        if (e == cudaSuccess) e = launch_unpack(tab, static_cast<cudaStream_t>(stream));
-      return e;
-    });
+  return entry(ctx, "adamw8_unpack", "mo adamw8_unpack", [&]() {
+    if (n == 0) return cudaSuccess;
+    return run_unpack(ctx, *build_moments(list, n), stream);
   });
 }
-
 mo_status clip_grads(mo_ctx* ctx, const mo_grad* list, int n, const mo_clip_cfg* cfg, void* stream) {
-  const char* who = "clip_grads";
-  if (ctx == nullptr) return MO_ERR_INVALID_ARG;
-  if (cfg == nullptr) return ctx_fail(ctx, MO_ERR_INVALID_ARG, "clip_grads: null cfg");
-  mo_status st = check_list(ctx, who, list, n, cfg);
-  if (st != MO_OK) return st;
-  ProfBind prof(ctx);
-  NvtxRange nvtx("mo clip_grads");
-  return guarded(ctx, who, [&](auto launch) {
-    if (!(cfg->max_norm >= 0.f)) refuse("max_norm must be >= 0");
-    if (cfg->norm == nullptr || cfg->factor == nullptr) refuse("null norm or factor");
-    if (!aligned(cfg->scale, 4) || !aligned(cfg->norm, 4) || !aligned(cfg->factor, 4) || !aligned(cfg->nonfinite, 4))
-      refuse("device scalars must be aligned to their type");
-    std::vector<Range> r;
-    r.reserve((size_t)n * 2 + 3);
-    add(r, cfg->norm, 4, true);
-    add(r, cfg->factor, 4, true);
-    add(r, cfg->nonfinite, 4, true);
-    add(r, cfg->scale, 4, false);
-    Tables tabs(true);
-    for (int i = 0; i < n; ++i) {
-      const mo_grad& a = list[i];
-      if (!numel_ok(a.numel, i) || a.G == nullptr) continue;
-      if (!type_ok(a.g_type) || (a.out != nullptr && !type_ok(a.out_type))) refuse("bad g_type or out_type" + at(i));
-      AwTensor t = {};
-      const bool in_place = cfg->apply && (a.out == nullptr || a.out == a.G);
-      if (in_place && a.out != nullptr && a.out_type != a.g_type) refuse("out in place must keep G's type" + at(i));
-      t.gt = (AwType)a.g_type;
-      buffer(r, a.G, a.numel, width(t.gt), in_place, "G", i);
-      t.G = a.G;
-      t.C = const_cast<void*>(a.G);
-      t.ct = t.gt;
-      t.vec = aligned(a.G, 8 * width(t.gt));
-      if (cfg->apply && !in_place) {
-        t.ct = (AwType)a.out_type;
-        buffer(r, a.out, a.numel, width(t.ct), true, "out", i);
-        t.C = a.out;
-        t.vec = t.vec && aligned(a.out, 8 * width(t.ct));
-      }
-      t.numel = a.numel;
-      t.index = (unsigned)i;
-      tabs.add(t);
-    }
-    check_apart(r);
-    tabs.finish();
-    size_t ws_bytes = 0;
-    char* ws = ctx_workspace(ctx, &ws_bytes);
-    if (ws == nullptr || ws_bytes < MO_CLIP_WORKSPACE_BYTES)
-      refuse("needs an attached workspace of MO_CLIP_WORKSPACE_BYTES", MO_ERR_NO_WORKSPACE);
-    ClipArgs a = {};
-    a.partial = reinterpret_cast<double*>(ws + WS_HEADER);
-    a.max_norm = cfg->max_norm;
-    a.scale = cfg->scale;
-    a.norm = cfg->norm;
-    a.factor = cfg->factor;
-    a.nonfinite = cfg->nonfinite;
-    // several tables share the fixed number of partial sums
-    const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const int each = tabs.all().empty() ? 0 : CLIP_MAX_CTAS / (int)tabs.all().size();
-    if (!tabs.all().empty() && each == 0) refuse("too many tensors");
-    return launch([&]() {
-      cudaError_t e = cudaSuccess;
-      for (const AwTable& tab : tabs.all()) {
-        if (e != cudaSuccess) break;
-        const int ctas = clip_norm_ctas(tab, each);
-        e = launch_clip_norm(tab, a.partial + a.parts, ctas, s);
-        a.parts += ctas;
-      }
-      if (e == cudaSuccess) e = launch_clip_finish(a, s);
-      if (cfg->apply)
-        for (const AwTable& tab : tabs.all())
-          if (e == cudaSuccess) e = launch_clip_scale(tab, cfg->factor, s);
-      return e;
-    });
-  });
+  return entry(ctx, "clip_grads", "mo clip_grads",
+               [&]() { return run_clip(ctx, *build_grads(list, n), given(cfg), stream); });
 }
 
 }  // extern "C"

@@ -170,7 +170,11 @@ def test_clip_refusals(lib, ctx, cfg, grad, word):
 class _Dev:
     """Stands in for a CUDA tensor (no GPU here)."""
 
+    place = 1 << 20
+
     def __init__(self, numel, dtype, device=0, contiguous=True, cuda=True):
+        _Dev.place += 1 << 16                 # buffers of a list must not overlap
+        self._at = _Dev.place
         self.is_cuda, self.dtype, self._n, self._c = cuda, dtype, numel, contiguous
         self.device = torch.device("cuda", device)
 
@@ -181,13 +185,11 @@ class _Dev:
         return self._n
 
     def data_ptr(self):
-        return 4096
+        return self._at
 
 
-def _context():
-    c = mo.Context.__new__(mo.Context)
-    c.device = 0
-    return c
+def _context(device=0):
+    return mo.Context(device)                 # host memory only
 
 
 def _mat(**kw):
@@ -201,11 +203,15 @@ def _mat8(**kw):
                      VS=_Dev(2, u)), **kw)
 
 
-def test_binding_checks_lists():
+def test_binding_checks_lists(lib):
     c, f = _context(), torch.float32
     good = c.adamw_tensors([_mat(), _mat(G=None, copy=_Dev(300, torch.float16), lr_scale=0.5, weight_decay=0.1)])
-    assert len(good) == 2 and good.array[0].g_type == _lib.BF16 and good.array[1].G is None
-    assert good.array[1].copy_type == _lib.F16 and good.array[1].weight_decay == ctypes.c_float(0.1).value
+    assert len(good) == 2 and good.handle
+    with pytest.raises(mo.MoError, match="weight_decay"):
+        c.adamw_tensors([_mat(weight_decay=-0.1)])
+    twice = _mat()
+    with pytest.raises(mo.MoError, match="overlap"):
+        c.adamw_tensors([twice, twice])
     for bad in (_mat(W=_Dev(300, torch.float16)), _mat(W=_Dev(300, f, contiguous=False)), _mat(W=_Dev(300, f, cuda=False)),
                 _mat(W=_Dev(300, f, device=1)), _mat(G=_Dev(299, f)), _mat(M=_Dev(300, torch.bfloat16)),
                 _mat(V=_Dev(301, f)), _mat(copy=_Dev(300, f)), _mat(copy=_Dev(3, torch.bfloat16))):
@@ -227,21 +233,47 @@ def test_binding_checks_lists():
             c.clip_tensors([bad])
 
 
-def test_binding_refuses_a_list_of_another_kind():
+def test_binding_refuses_a_list_of_another_kind(lib):
     c = _context()
     grads = c.clip_tensors([_Dev(5, torch.float32)])
     with pytest.raises(ValueError, match="'adamw'"):
         c._list("adamw", grads)
-    other = _context()
-    other.device = 1
     with pytest.raises(ValueError, match="cuda:1"):
-        other._list("grads", grads)
+        _context(1)._list("grads", grads)
+
+
+def test_prepared_lists(lib, ctx):
+    """Lists refuse what the calls with arrays refuse, and the calls a list of another kind."""
+    out = ctypes.c_void_p(5)
+    arr = (_lib.AdamWTensor * 2)(_tensor(), _tensor())
+    assert lib.mo_adamw_list(ctx, arr, 2, ctypes.byref(out)) == BAD and not out.value
+    assert b"overlap" in lib.mo_last_error(ctx)
+    assert lib.mo_adamw_list(ctx, None, 1, ctypes.byref(out)) == BAD and lib.mo_adamw_list(ctx, arr, -1, ctypes.byref(out)) == BAD
+    assert lib.mo_adamw_list(ctx, arr, 1, None) == BAD
+    assert lib.mo_adamw_list(ctx, arr, 1, ctypes.byref(out)) == 0 and out.value
+    cfg, pack = _cfg(), _lib.PackCfg()
+    clip = _lib.ClipCfg(1.0, 1, None, 16, 32, None)
+    assert lib.adamw_step_list(ctx, out, ctypes.byref(_cfg(beta1=2.0)), 1, None) == BAD
+    assert lib.adamw_step_list(ctx, out, None, 1, None) == BAD
+    for st in (lib.adamw8_step_list(ctx, out, ctypes.byref(cfg), 1, None), lib.adamw8_pack_list(ctx, out, ctypes.byref(pack), None),
+               lib.adamw8_unpack_list(ctx, out, None), lib.clip_grads_list(ctx, out, ctypes.byref(clip), None)):
+        assert st == BAD and b"another call" in lib.mo_last_error(ctx)
+    assert lib.adamw_step_list(ctx, None, ctypes.byref(cfg), 1, None) == BAD
+    lib.mo_list_destroy(out)
+    lib.mo_list_destroy(None)
+    # scalars of a clip inside a gradient
+    grads = (_lib.Grad * 1)(_lib.Grad(100, 1 << 20, None, 0, 0))
+    assert lib.mo_grad_list(ctx, grads, 1, ctypes.byref(out)) == 0
+    clip = _lib.ClipCfg(1.0, 1, None, (1 << 20) + 396, 32, None)
+    assert lib.clip_grads_list(ctx, out, ctypes.byref(clip), None) == BAD and b"overlap" in lib.mo_last_error(ctx)
+    lib.mo_list_destroy(out)
 
 
 def test_scalars():
     from matrix_aware_optimizers_muon_b200 import _scalar
     assert _scalar(None, "x", 0, torch.float32) is None
-    assert _scalar(_Dev(1, torch.float32), "x", 0, torch.float32) == 4096
+    one = _Dev(1, torch.float32)
+    assert _scalar(one, "x", 0, torch.float32) == one.data_ptr()
     for bad in (_Dev(2, torch.float32), _Dev(1, torch.float64), _Dev(1, torch.float32, cuda=False), _Dev(1, torch.float32, device=1)):
         with pytest.raises(ValueError, match="grad_scale"):
             _scalar(bad, "grad_scale", 0, torch.float32)

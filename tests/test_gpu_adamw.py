@@ -333,7 +333,7 @@ def test_unpack_every_code_and_scale():
     codes = torch.arange(256, dtype=torch.uint8, device="cuda").repeat(255)
     scales = torch.arange(255, dtype=torch.uint8, device="cuda")        # 255 stands for no number
     m, v = (torch.empty(codes.numel(), device="cuda") for _ in range(2))
-    ctx.adamw8_unpack([dict(M=m, V=v, M8=codes, V8=codes, MS=scales, VS=scales)])
+    ctx.adamw8_unpack([dict(M=m, V=v, M8=codes, V8=codes.clone(), MS=scales, VS=scales.clone())])
     c, s = codes.cpu().numpy(), scales.cpu().numpy()
     with np.errstate(over="ignore"):
         np.testing.assert_array_equal(m.cpu().numpy(), oa.first_moment(c, s).astype(np.float32))
