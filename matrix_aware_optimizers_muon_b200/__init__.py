@@ -135,6 +135,7 @@ class Context:
         import torch
         self.lib = _lib.load()
         self.device = torch.cuda.current_device() if device is None else int(device)
+        self._device = torch.device("cuda", self.device)
         h = c_void_p()
         st = self.lib.mo_ctx_create(byref(h), self.device)
         if st != 0:
@@ -558,8 +559,11 @@ class Context:
         grads = self._list("grads", grads)
         if reserve and (self._workspace is None or self._workspace.numel() < _lib.CLIP_WORKSPACE_BYTES):
             self.attach_workspace(_lib.CLIP_WORKSPACE_BYTES, stream)
-        with torch.cuda.stream(stream):     # the scalars belong to the stream that writes them
-            norm, factor = torch.empty(2, dtype=torch.float32, device=f"cuda:{self.device}").unbind()
+        if stream is None:
+            norm, factor = torch.empty(2, dtype=torch.float32, device=self._device).unbind()
+        else:
+            with torch.cuda.stream(stream):     # the scalars belong to the stream that writes them
+                norm, factor = torch.empty(2, dtype=torch.float32, device=self._device).unbind()
         at = norm.data_ptr()
         cfg = ClipCfg(max_norm, bool(apply), _scalar(scale, "scale", self.device, torch.float32), at, at + 4,
                       _scalar(nonfinite, "nonfinite", self.device, torch.int32))

@@ -30,13 +30,15 @@ namespace {
 
 constexpr int PER = AW_BLOCK / 32;     // elements of a lane
 // CTAs (warps) of a step on one SM: five for each of its four schedulers, at 96
-// registers.  16 and 24 take 7 and 8 % longer, 21 as long as 24 would: a
-// scheduler with one warp more than the others finishes last.
+// registers.  16 and 24 take 12 and 7 % longer (8 bits), 21 as long as 24 would:
+// a scheduler with one warp more than the others finishes last.  Without two
+// buffers (shifted) 28 are best: 202 us for 54 M bf16 elements, 225 with 20.
 constexpr int STEP_CTAS = 20;
+constexpr int SHIFTED_CTAS = 28;
 
-// A lane's place in a block: wide lanes hold 8 neighbours, narrow ones elements
-// 32 apart.
-template <bool WIDE>
+// A lane's place in a block: wide lanes (1) and shifted ones (2) hold 8
+// neighbours, narrow ones (0) elements 32 apart.
+template <int WIDE>
 struct Place {
   unsigned long long first;   // the lane's first element
   int left;                   // narrow: elements of the tensor from there on
@@ -60,6 +62,7 @@ template <typename T>
 struct Raw {
   static constexpr int WORDS = PER * sizeof(T) / 4;
   unsigned w[WORDS];
+  uint4 behind;                // shifted: the 16 bytes behind
 };
 
 __device__ __forceinline__ unsigned bits_of(float x) { return __float_as_uint(x); }
@@ -99,10 +102,140 @@ __device__ __forceinline__ void store_words(const unsigned (&w)[2], void* p) {
   asm volatile("st.global.v2.b32 [%0], {%1, %2};" ::"l"(p), "r"(w[0]), "r"(w[1]) : "memory");
 }
 
+// Shifted accesses: 8 neighbours of a lane at an address that is aligned to its
+// elements alone.  A lane reads the 16-byte words that its elements begin in and
+// the one behind, which L1 holds for the next lane; it writes the words that
+// begin before its elements' end, with what the lane before has of them.  The
+// words at the two ends of a block hold elements of its neighbours too: a block
+// goes this way only where both neighbours (8 elements of the next) are in the
+// tensor, and those words are written by elements.
+template <int BY>
+__device__ __forceinline__ void shift_words(unsigned (&w)[8], const unsigned (&c)[12]) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) w[k] = c[k + BY];
+}
+
+template <int BY>
+__device__ __forceinline__ void shift_words(unsigned (&w)[4], const unsigned (&c)[8], unsigned bits) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) w[k] = __funnelshift_r(c[k + BY], c[k + BY + 1], bits);
+}
+
+// The aligned words around a lane's elements ...
+template <int WORDS>
+__device__ __forceinline__ void load_around(unsigned (&w)[WORDS], uint4& behind, const void* p) {
+  const unsigned d = (unsigned)(reinterpret_cast<uintptr_t>(p) & 15u);
+  const uint4* a = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(p) - d);
+#pragma unroll
+  for (int k = 0; k < WORDS / 4; ++k) {
+    const uint4 x = a[k];
+    w[4 * k] = x.x;
+    w[4 * k + 1] = x.y;
+    w[4 * k + 2] = x.z;
+    w[4 * k + 3] = x.w;
+  }
+  behind = make_uint4(0, 0, 0, 0);
+  if (d != 0) behind = a[WORDS / 4];
+}
+
+// ... and the elements out of them.
+__device__ __forceinline__ void settle(unsigned (&w)[8], const uint4& z, const void* p) {
+  const unsigned d = (unsigned)(reinterpret_cast<uintptr_t>(p) & 15u);
+  const unsigned c[12] = {w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7], z.x, z.y, z.z, z.w};
+  switch (d >> 2) {
+    case 0: shift_words<0>(w, c); break;
+    case 1: shift_words<1>(w, c); break;
+    case 2: shift_words<2>(w, c); break;
+    default: shift_words<3>(w, c); break;
+  }
+}
+
+__device__ __forceinline__ void settle(unsigned (&w)[4], const uint4& z, const void* p) {
+  const unsigned d = (unsigned)(reinterpret_cast<uintptr_t>(p) & 15u);
+  const unsigned c[8] = {w[0], w[1], w[2], w[3], z.x, z.y, z.z, z.w};
+  const unsigned bits = (d & 2u) * 8u;
+  switch (d >> 2) {
+    case 0: shift_words<0>(w, c, bits); break;
+    case 1: shift_words<1>(w, c, bits); break;
+    case 2: shift_words<2>(w, c, bits); break;
+    default: shift_words<3>(w, c, bits); break;
+  }
+}
+
+// A fetched lane's elements in order: nothing to do unless they came shifted.
+template <int WIDE, typename T>
+__device__ __forceinline__ Raw<T> settled(const Raw<T>& r, const T* p) {
+  Raw<T> s = r;
+  if constexpr (WIDE == 2 && sizeof(T) > 1) settle(s.w, s.behind, p);
+  return s;
+}
+
+__device__ __forceinline__ unsigned up(unsigned x) { return __shfl_up_sync(0xffffffffu, x, 1); }
+
+template <int BY>
+__device__ __forceinline__ void put_shifted(const unsigned (&w)[8], const unsigned (&before)[8], unsigned* p) {
+  unsigned o[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) o[k] = k < BY ? before[8 - BY + k] : w[k - BY];
+  uint4* a = reinterpret_cast<uint4*>(p - BY);
+  if (threadIdx.x != 0 || BY == 0) {
+    a[0] = make_uint4(o[0], o[1], o[2], o[3]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4 - BY; ++k) p[k] = w[k];
+  }
+  a[1] = make_uint4(o[4], o[5], o[6], o[7]);
+  if (threadIdx.x == 31) {
+#pragma unroll
+    for (int k = 8 - BY; k < 8; ++k) p[k] = w[k];
+  }
+}
+
+__device__ __forceinline__ void store_shifted(const unsigned (&w)[8], void* to) {
+  unsigned* p = static_cast<unsigned*>(to);
+  unsigned before[8] = {};
+#pragma unroll
+  for (int k = 5; k < 8; ++k) before[k] = up(w[k]);
+  switch ((reinterpret_cast<uintptr_t>(p) >> 2) & 3u) {
+    case 0: put_shifted<0>(w, before, p); break;
+    case 1: put_shifted<1>(w, before, p); break;
+    case 2: put_shifted<2>(w, before, p); break;
+    default: put_shifted<3>(w, before, p); break;
+  }
+}
+
+template <int BY>
+__device__ __forceinline__ void shift_up(unsigned (&o)[4], const unsigned (&c)[8], bool odd) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) o[k] = odd ? __funnelshift_l(c[3 + k - BY], c[4 + k - BY], 16) : c[4 + k - BY];
+}
+
+__device__ __forceinline__ void store_shifted(const unsigned (&w)[4], void* to) {
+  unsigned short* p = static_cast<unsigned short*>(to);
+  const int by = (int)(reinterpret_cast<uintptr_t>(p) >> 1) & 7;       // elements
+  const unsigned c[8] = {up(w[0]), up(w[1]), up(w[2]), up(w[3]), w[0], w[1], w[2], w[3]};
+  unsigned o[4];
+  switch (by >> 1) {
+    case 0: shift_up<0>(o, c, by & 1); break;
+    case 1: shift_up<1>(o, c, by & 1); break;
+    case 2: shift_up<2>(o, c, by & 1); break;
+    default: shift_up<3>(o, c, by & 1); break;
+  }
+  if (threadIdx.x != 0 || by == 0) *reinterpret_cast<uint4*>(p - by) = make_uint4(o[0], o[1], o[2], o[3]);
+  if (by != 0 && (threadIdx.x == 0 || threadIdx.x == 31)) {
+    // the first lane's elements in the word that the block begins in, the last lane's in the one behind
+#pragma unroll
+    for (int j = 0; j < PER; ++j)
+      if ((j < PER - by) == (threadIdx.x == 0)) p[j] = (unsigned short)(w[j / 2] >> (16 * (j % 2)));
+  }
+}
+
 // p is the lane's first element; a wide lane may read AT blocks further on.
-template <bool WIDE, int AT = 0, typename T>
+template <int WIDE, int AT = 0, typename T>
 __device__ __forceinline__ void fetch(Raw<T>& r, const T* p, const Place<WIDE>& b) {
-  if (WIDE) {
+  if constexpr (WIDE == 2 && sizeof(T) > 1) {
+    load_around(r.w, r.behind, p + AT * AW_BLOCK);
+  } else if constexpr (WIDE > 0) {
     load_words<AT * AW_BLOCK * (int)sizeof(T)>(r.w, p);
   } else {
     constexpr int IN = 4 / sizeof(T);                  // elements of a word
@@ -116,9 +249,11 @@ __device__ __forceinline__ void fetch(Raw<T>& r, const T* p, const Place<WIDE>& 
   }
 }
 
-template <bool WIDE, typename T>
+template <int WIDE, typename T>
 __device__ __forceinline__ void put(const Raw<T>& r, T* p, const Place<WIDE>& b) {
-  if (WIDE) {
+  if constexpr (WIDE == 2 && sizeof(T) > 1) {
+    store_shifted(r.w, p);
+  } else if constexpr (WIDE > 0) {
     store_words(r.w, p);
   } else {
     constexpr int IN = 4 / sizeof(T);
@@ -172,7 +307,7 @@ __device__ __forceinline__ void narrow_all(Raw<__half>& r, const float (&x)[PER]
   }
 }
 
-template <bool WIDE, typename T>
+template <int WIDE, typename T>
 __device__ __forceinline__ void store(const float (&x)[PER], T* p, const Place<WIDE>& b) {
   Raw<T> r;
   narrow_all(r, x);
@@ -192,19 +327,59 @@ __device__ __forceinline__ int find(const AwTableOf<N>& tab, unsigned run, int i
   return lo;
 }
 
-template <typename Op, int... K>
+template <int WIDE, typename Op, int... K>
 __device__ __forceinline__ void fetch_all(const Op& op, typename Op::Load (&in)[sizeof...(K)], unsigned at,
                                           std::integer_sequence<int, K...>) {
-  (op.template fetch<K>(in[K], at), ...);
+  (op.template fetch<K, WIDE>(in[K], at), ...);
+}
+
+// Blocks [r, end) of a run.  With BATCH 0 a block is fetched while the one before
+// is worked on, in two buffers and two copies of the body so that nothing moves
+// between them; else BATCH blocks are fetched and then worked on.
+template <int WIDE, typename Op>
+__device__ __forceinline__ void work_blocks(Op& op, unsigned long long first, int r, int end) {
+  unsigned at = (unsigned)r * AW_BLOCK + threadIdx.x * PER;
+  const auto work = [&](const typename Op::Load& in) {
+    op.work(in, Place<WIDE>{first + at, 0}, at, r);
+    at += AW_BLOCK;
+    ++r;
+  };
+  // two shifted buffers take more registers than a step has
+  constexpr int BATCH = Op::BATCH == 0 && WIDE == 2 ? 1 : Op::BATCH;
+  if constexpr (BATCH > 0) {
+    while (BATCH > 1 && r + BATCH <= end) {
+      typename Op::Load in[BATCH];
+      fetch_all<WIDE>(op, in, at, std::make_integer_sequence<int, BATCH>());
+#pragma unroll
+      for (int k = 0; k < BATCH; ++k) work(in[k]);
+    }
+    while (r < end) {
+      typename Op::Load in;
+      op.template fetch<0, WIDE>(in, at);
+      work(in);
+    }
+  } else if (r < end) {
+    typename Op::Load even, odd;
+    op.template fetch<0, WIDE>(even, at);
+    while (true) {
+      if (r + 1 < end) op.template fetch<1, WIDE>(odd, at);
+      work(even);
+      if (r == end) break;
+      if (r + 1 < end) op.template fetch<1, WIDE>(even, at);
+      work(odd);
+      if (r == end) break;
+    }
+  }
 }
 
 // A CTA is one warp.  It takes every gridDim-th run of tab.run blocks of a
-// tensor.  With BATCH 0 it fetches a block while it works on the one before,
-// else it fetches BATCH blocks and then works on them.
+// tensor.
 //   Op::start(tensor, first element, blocks)   a run begins
 //   Op::fetch<AT>(Load&, at)                   reads a whole block, AT blocks behind the lane's offset `at`
 //   Op::work(Load, Place, at, r)               works on block r of the run
-//   Op::narrow(tensor, Place, at, r)           reads and works on block r of a misaligned tensor (VEC false) or a partial one
+//   Op::narrow(tensor, Place, at, r)           reads and works on a partial block r, or one that has no other way
+// With VEC all tensors are aligned; without, their blocks are read shifted
+// where that is possible (t.vec), and narrow at their ends.
 //   Op::finish(blocks)                         the run ends
 template <bool VEC, int N, typename Op>
 __device__ __forceinline__ void walk(const AwTableOf<N>& tab, Op& op) {
@@ -217,44 +392,22 @@ __device__ __forceinline__ void walk(const AwTableOf<N>& tab, Op& op) {
     const long long block = (long long)(run - t.first) * tab.run;
     const unsigned long long first = (unsigned long long)block * AW_BLOCK;
     const int blocks = (int)min((long long)tab.run, (t.numel + AW_BLOCK - 1) / AW_BLOCK - block);
-    const int whole = VEC ? (int)min((long long)blocks, t.numel / AW_BLOCK - block) : 0;
-    op.start(t, first, blocks);
-    int r = 0;
-    unsigned at = lane * PER;
-    if constexpr (Op::BATCH > 0) {
-      for (; r + Op::BATCH <= whole; r += Op::BATCH) {
-        typename Op::Load in[Op::BATCH];
-        fetch_all(op, in, at, std::make_integer_sequence<int, Op::BATCH>());
-#pragma unroll
-        for (int k = 0; k < Op::BATCH; ++k) {
-          op.work(in[k], Place<true>{first + at, 0}, at, r + k);
-          at += AW_BLOCK;
-        }
-      }
-      for (; r < whole; ++r) {
-        typename Op::Load in;
-        op.template fetch<0>(in, at);
-        op.work(in, Place<true>{first + at, 0}, at, r);
-        at += AW_BLOCK;
-      }
-    } else if (whole > 0) {
-      typename Op::Load even, odd;             // two buffers and two copies of the body: no moves between them
-      op.template fetch<0>(even, at);
-      while (true) {
-        if (r + 1 < whole) op.template fetch<1>(odd, at);
-        op.work(even, Place<true>{first + at, 0}, at, r);
-        at += AW_BLOCK;
-        if (++r == whole) break;
-        if (r + 1 < whole) op.template fetch<1>(even, at);
-        op.work(odd, Place<true>{first + at, 0}, at, r);
-        at += AW_BLOCK;
-        if (++r == whole) break;
-      }
+    // blocks [from, to) are whole (VEC), or have both neighbours: the tensor's first has none before it
+    int from = 0, to = 0;
+    if (VEC) {
+      to = (int)min((long long)blocks, t.numel / AW_BLOCK - block);
+    } else if (t.vec) {
+      from = block == 0 ? 1 : 0;
+      to = (int)max((long long)from, min((long long)blocks, (t.numel - 8) / AW_BLOCK - block));
     }
-    for (; r < blocks; ++r) {
+    op.start(t, first, blocks);
+    work_blocks<VEC ? 1 : 2>(op, first, from, to);
+    for (int r = 0; r < blocks; ++r) {
+      if (r == from) r = to;
+      if (r >= blocks) break;
       const unsigned at = (unsigned)r * AW_BLOCK + lane;
       const long long left = t.numel - (long long)(first + at);
-      op.narrow(t, Place<false>{first + at, left < AW_BLOCK ? (int)left : AW_BLOCK}, at, r);
+      op.narrow(t, Place<0>{first + at, left < AW_BLOCK ? (int)left : AW_BLOCK}, at, r);
     }
     op.finish(blocks);
   }
@@ -299,7 +452,7 @@ __device__ __forceinline__ unsigned second_word(unsigned first, Keys k) {
 
 // The first words that a lane's elements need: wide lanes hold whole pairs,
 // narrow ones an element of each.
-template <bool WIDE>
+template <int WIDE>
 struct Noise {
   unsigned w[WIDE ? PER / 2 : PER];
   __device__ __forceinline__ void draw(const Place<WIDE>& b, Keys k) {
@@ -405,7 +558,7 @@ __device__ __forceinline__ unsigned pack_tops(unsigned a, unsigned b, unsigned c
 }
 
 // Codes of v in bits 24 to 31 of r; scaled is v times 2^(127 - s) 2^-112.
-template <bool STOCHASTIC, bool WIDE>
+template <bool STOCHASTIC, int WIDE>
 __device__ __forceinline__ void second_codes(unsigned (&r)[PER], const float (&v)[PER], const float (&scaled)[PER],
                                              const Noise<WIDE>& n) {
   unsigned least = 0xffffffffu;
@@ -422,7 +575,7 @@ __device__ __forceinline__ void second_codes(unsigned (&r)[PER], const float (&v
   }
 }
 
-template <bool WIDE>
+template <int WIDE>
 __device__ __forceinline__ void store_moments(float (&m)[PER], float (&v)[PER], Code* mp, Code* vp, Scales& scales, int r,
                                               const Place<WIDE>& b, bool stochastic, const Noise<WIDE>& n) {
   float bm = 0.f;
@@ -473,8 +626,8 @@ __device__ __forceinline__ void store_moments(float (&m)[PER], float (&v)[PER], 
     for (int j = 0; j < PER; ++j)
       if (odd & (1u << j)) vr[j] = 255u << 24;
   }
-  put(Raw<Code>{{__byte_perm(mw[0], mw[1], 0x5410), __byte_perm(mw[2], mw[3], 0x5410)}}, mp, b);
-  put(Raw<Code>{{pack_tops(vr[0], vr[1], vr[2], vr[3]), pack_tops(vr[4], vr[5], vr[6], vr[7])}}, vp, b);
+  put(Raw<Code>{{__byte_perm(mw[0], mw[1], 0x5410), __byte_perm(mw[2], mw[3], 0x5410)}, {}}, mp, b);
+  put(Raw<Code>{{pack_tops(vr[0], vr[1], vr[2], vr[3]), pack_tops(vr[4], vr[5], vr[6], vr[7])}, {}}, vp, b);
   scales.set(r, ms, vs);
 }
 
@@ -545,7 +698,7 @@ __device__ __forceinline__ void update(float (&w)[PER], float (&m)[PER], float (
 
 // bf16 weights without an fp32 master: to the neighbour above with the
 // probability of the distance, so that updates below half a step are not lost
-template <bool WIDE>
+template <int WIDE>
 __device__ __forceinline__ void round_weights(Raw<__nv_bfloat16>& out, const float (&w)[PER], const Noise<WIDE>& n) {
   float zero = 0.f;                                    // NaN when a weight is not finite
 #pragma unroll
@@ -601,7 +754,7 @@ __device__ __forceinline__ void moments_of(float (&m)[PER], float (&v)[PER], con
   }
 }
 
-template <bool EIGHT, typename WT, typename GT, bool VEC>
+template <bool EIGHT, typename WT, typename GT>
 struct StepOp {
   static constexpr int BATCH = 0;
   static constexpr bool BACKWARDS = false;
@@ -637,21 +790,21 @@ struct StepOp {
       scales.load(ms, vs, blocks);
     }
   }
-  template <int AT, bool WIDE = true>
+  template <int AT, int WIDE = 1>
   __device__ __forceinline__ void fetch(Load& in, unsigned at, const Place<WIDE>& b = {}) const {
     mo::fetch<WIDE, AT>(in.g, g + at, b);
     mo::fetch<WIDE, AT>(in.w, w + at, b);
     mo::fetch<WIDE, AT>(in.m, m + at, b);
     mo::fetch<WIDE, AT>(in.v, v + at, b);
   }
-  template <bool WIDE>
+  template <int WIDE>
   __device__ __forceinline__ void work(const Load& in, const Place<WIDE>& b, unsigned at, int r) {
     float w1[PER], g1[PER], m1[PER], v1[PER];
-    widen_all(g1, in.g);
-    widen_all(w1, in.w);
+    widen_all(g1, settled<WIDE>(in.g, g + at));
+    widen_all(w1, settled<WIDE>(in.w, w + at));
     if (h.gscale != nullptr) scale_all(g1, gs);
     float sm = 1.f, sv = 1.f;
-    moments_of(m1, v1, in.m, in.v, sm, sv, EIGHT ? scales.of(r) : 0);
+    moments_of(m1, v1, settled<WIDE>(in.m, m + at), settled<WIDE>(in.v, v + at), sm, sv, EIGHT ? scales.of(r) : 0);
     update(w1, m1, v1, g1, h, s.r, sm, sv);
     constexpr bool LOW = sizeof(WT) == 2;
     Noise<WIDE> n;
@@ -673,42 +826,41 @@ struct StepOp {
       store(w1, w + at, b);
     }
   }
-  __device__ __forceinline__ void work_narrow(const Place<false>& b, unsigned at, int r) {
+  __device__ __forceinline__ void work_narrow(const Place<0>& b, unsigned at, int r) {
     Load in;
-    fetch<0, false>(in, at, b);
+    fetch<0, 0>(in, at, b);
     work(in, b, at, r);
   }
-  __device__ __forceinline__ void narrow(const AwTensor& t, const Place<false>& b, unsigned at, int r);
+  __device__ __forceinline__ void narrow(const AwTensor& t, const Place<0>& b, unsigned at, int r);
   __device__ __forceinline__ void finish(int blocks) const {
     if (EIGHT) scales.store(ms, vs, blocks);
   }
 };
 
-// The partial block of an aligned tensor, apart from the registers of the main
-// path; returns the run's scales.
+// A narrow block, apart from the registers of the main path; returns the run's
+// scales.
 template <bool EIGHT, typename WT, typename GT>
 __device__ __noinline__ unsigned step_tail(const AwTensor& t, const AwHyper& h, float gs, unsigned long long first, int left,
                                            unsigned scales, int r) {
-  StepOp<EIGHT, WT, GT, false> op(h, gs);
+  StepOp<EIGHT, WT, GT> op(h, gs);
   op.point(t, first - threadIdx.x);
   op.scales.all = scales;
-  op.work_narrow(Place<false>{first, left}, threadIdx.x, r);
+  op.work_narrow(Place<0>{first, left}, threadIdx.x, r);
   return op.scales.all;
 }
 
-template <bool EIGHT, typename WT, typename GT, bool VEC>
-__device__ __forceinline__ void StepOp<EIGHT, WT, GT, VEC>::narrow(const AwTensor& t, const Place<false>& b, unsigned at, int r) {
-  if (VEC) scales.all = step_tail<EIGHT, WT, GT>(t, h, gs, b.first, b.left, EIGHT ? scales.all : 0, r);
-  else work_narrow(b, at, r);
+template <bool EIGHT, typename WT, typename GT>
+__device__ __forceinline__ void StepOp<EIGHT, WT, GT>::narrow(const AwTensor& t, const Place<0>& b, unsigned, int r) {
+  scales.all = step_tail<EIGHT, WT, GT>(t, h, gs, b.first, b.left, EIGHT ? scales.all : 0, r);
 }
 
 template <bool EIGHT, typename WT, typename GT, bool VEC, int N>
-__global__ void __launch_bounds__(AW_THREADS, STEP_CTAS)
+__global__ void __launch_bounds__(AW_THREADS, VEC ? STEP_CTAS : SHIFTED_CTAS)
     adamw_kernel(const __grid_constant__ AwTableOf<N> tab, const __grid_constant__ AwHyper h) {
   pdl_wait();
   pdl_trigger();
   if (h.skip != nullptr && *h.skip != 0) return;
-  StepOp<EIGHT, WT, GT, VEC> op(h, h.gscale ? *h.gscale : 1.f);
+  StepOp<EIGHT, WT, GT> op(h, h.gscale ? *h.gscale : 1.f);
   walk<VEC>(tab, op);
 }
 
@@ -740,23 +892,23 @@ struct PackOp {
     if (h.stochastic) k = keys_of(h, t.index);
     scales.all = 0;
   }
-  template <int AT, bool WIDE = true>
+  template <int AT, int WIDE = 1>
   __device__ __forceinline__ void fetch(Load& in, unsigned at, const Place<WIDE>& b = {}) const {
     mo::fetch<WIDE, AT>(in.m, m + at, b);
     mo::fetch<WIDE, AT>(in.v, v + at, b);
   }
-  template <bool WIDE>
+  template <int WIDE>
   __device__ __forceinline__ void work(const Load& in, const Place<WIDE>& b, unsigned at, int r) {
     float x[PER], y[PER];
-    widen_all(x, in.m);
-    widen_all(y, in.v);
+    widen_all(x, settled<WIDE>(in.m, m + at));
+    widen_all(y, settled<WIDE>(in.v, v + at));
     Noise<WIDE> n;
     if (h.stochastic) n.draw(b, k);
     store_moments(x, y, m8 + at, v8 + at, scales, r, b, h.stochastic != 0, n);
   }
-  __device__ __forceinline__ void narrow(const AwTensor&, const Place<false>& b, unsigned at, int r) {
+  __device__ __forceinline__ void narrow(const AwTensor&, const Place<0>& b, unsigned at, int r) {
     Load in;
-    fetch<0, false>(in, at, b);
+    fetch<0, 0>(in, at, b);
     work(in, b, at, r);
   }
   __device__ __forceinline__ void finish(int blocks) const { scales.store(ms, vs, blocks); }
@@ -790,12 +942,12 @@ struct UnpackOp {
     v = static_cast<T*>(t.C) + first;
     scales.load(t.MS + first / AW_BLOCK, t.VS + first / AW_BLOCK, blocks);
   }
-  template <int AT, bool WIDE = true>
+  template <int AT, int WIDE = 1>
   __device__ __forceinline__ void fetch(Load& in, unsigned at, const Place<WIDE>& b = {}) const {
     mo::fetch<WIDE, AT>(in.m, m8 + at, b);
     mo::fetch<WIDE, AT>(in.v, v8 + at, b);
   }
-  template <bool WIDE>
+  template <int WIDE>
   __device__ __forceinline__ void work(const Load& in, const Place<WIDE>& b, unsigned at, int r) const {
     float x[PER], y[PER];
     decode(x, y, in.m, in.v);
@@ -806,9 +958,9 @@ struct UnpackOp {
     store(x, m + at, b);
     store(y, v + at, b);
   }
-  __device__ __forceinline__ void narrow(const AwTensor&, const Place<false>& b, unsigned at, int r) const {
+  __device__ __forceinline__ void narrow(const AwTensor&, const Place<0>& b, unsigned at, int r) const {
     Load in;
-    fetch<0, false>(in, at, b);
+    fetch<0, 0>(in, at, b);
     work(in, b, at, r);
   }
   __device__ __forceinline__ void finish(int) const {}
@@ -842,19 +994,19 @@ struct NormOp {
   double sum = 0.0;
   const T* g;
   __device__ __forceinline__ void start(const AwTensor& t, unsigned long long first, int) { g = static_cast<const T*>(t.G) + first; }
-  template <int AT, bool WIDE = true>
+  template <int AT, int WIDE = 1>
   __device__ __forceinline__ void fetch(Load& in, unsigned at, const Place<WIDE>& b = {}) const { mo::fetch<WIDE, AT>(in, g + at, b); }
-  template <bool WIDE>
-  __device__ __forceinline__ void work(const Load& in, const Place<WIDE>&, unsigned, int) {
+  template <int WIDE>
+  __device__ __forceinline__ void work(const Load& in, const Place<WIDE>&, unsigned at, int) {
     float x[PER], s = 0.f;
-    widen_all(x, in);
+    widen_all(x, settled<WIDE>(in, g + at));
 #pragma unroll
     for (int j = 0; j < PER; ++j) s = fmaf(x[j], x[j], s);
     sum += (double)s;
   }
-  __device__ __forceinline__ void narrow(const AwTensor&, const Place<false>& b, unsigned at, int r) {
+  __device__ __forceinline__ void narrow(const AwTensor&, const Place<0>& b, unsigned at, int r) {
     Load in;
-    fetch<0, false>(in, at, b);
+    fetch<0, 0>(in, at, b);
     work(in, b, at, r);
   }
   __device__ __forceinline__ void finish(int) const {}
@@ -923,18 +1075,18 @@ struct ScaleOp {
     g = static_cast<const T*>(t.G) + first;
     out = static_cast<OUT*>(t.C) + first;
   }
-  template <int AT, bool WIDE = true>
+  template <int AT, int WIDE = 1>
   __device__ __forceinline__ void fetch(Load& in, unsigned at, const Place<WIDE>& b = {}) const { mo::fetch<WIDE, AT>(in, g + at, b); }
-  template <bool WIDE>
+  template <int WIDE>
   __device__ __forceinline__ void work(const Load& in, const Place<WIDE>& b, unsigned at, int) const {
     float x[PER];
-    widen_all(x, in);
+    widen_all(x, settled<WIDE>(in, g + at));
     scale_all(x, f);
     store(x, out + at, b);
   }
-  __device__ __forceinline__ void narrow(const AwTensor&, const Place<false>& b, unsigned at, int r) const {
+  __device__ __forceinline__ void narrow(const AwTensor&, const Place<0>& b, unsigned at, int r) const {
     Load in;
-    fetch<0, false>(in, at, b);
+    fetch<0, 0>(in, at, b);
     work(in, b, at, r);
   }
   __device__ __forceinline__ void finish(int) const {}
@@ -966,7 +1118,7 @@ using Pointee = typename std::remove_pointer<P>::type;
 
 // Launches one of four forms of a kernel: for aligned tensors or others, with a
 // short or a full table (its first AW_SHORT tensors are all that the short form
-// reads; 26 KB of parameters cost a launch 1.1 us more than 6).  The further
+// reads; 31 KB of parameters cost a launch 1.5 us more than 8).  The further
 // argument is passed by its address, like the table, and copied once.
 template <typename Arg>
 cudaError_t launch_list(const void* (&forms)[2][2], int kind, const AwTable& t, unsigned grid, const Arg& arg, cudaStream_t s) {
@@ -981,7 +1133,7 @@ cudaError_t launch_list(const void* (&forms)[2][2], int kind, const AwTable& t, 
   cfg.attrs = attr;
   cfg.numAttrs = pdl_off() ? 0 : 1;
   void* args[] = {const_cast<AwTable*>(&t), const_cast<Arg*>(&arg)};
-  return cudaLaunchKernelExC(&cfg, forms[t.t[0].vec != 0][t.n > AW_SHORT], args);
+  return cudaLaunchKernelExC(&cfg, forms[t.t[0].vec == 2][t.n > AW_SHORT], args);
 }
 #define MO_FORMS(KERNEL, ...)                                                                                       \
   {{(const void*)KERNEL<__VA_ARGS__, false, AW_SHORT>, (const void*)KERNEL<__VA_ARGS__, false, AW_MAX>},            \
@@ -1011,7 +1163,7 @@ cudaError_t launch_step(const AwTable& t, const AwHyper& h, cudaStream_t s) {
 // 1, 903 with 2, 951 with 8.
 int run_of(long long blocks, int most) {
   int run = 1;
-  while (run < most && blocks >= 16ll * run * device_sm_count()) run *= 2;
+  while (run < most && blocks >= 64ll * run * device_sm_count()) run *= 2;
   return run;
 }
 

@@ -14,12 +14,12 @@ constexpr int AW_THREADS = 32;     // a CTA is one warp, which works on one bloc
 constexpr int AW_RUN = 8;          // most blocks of a run (fp32 moments: AW_RUN32)
 constexpr int AW_RUN32 = 2;
 constexpr int AW_MAX = 350;        // tensors per launch (the table travels in the kernel's parameters)
-constexpr int AW_SHORT = 64;       // tensors that a launch with fewer parameters takes
+constexpr int AW_SHORT = 96;       // tensors that a launch with fewer parameters takes
 
 enum AwType : unsigned char { AW_F32 = 0, AW_BF16 = 1, AW_F16 = 2, AW_NONE = 3 };
 
-// One tensor.  All tensors of a table have the types and the alignment (vec) of
-// the first.  Which pointers are used depends on the kernel:
+// One tensor.  All tensors of a table have the types of the first, and either
+// all of them or none have vec 2.  Which pointers are used depends on the kernel:
 //   adamw    W, G, M, V (fp32), C (optional low-precision copy of W)
 //   adamw8   W, G, M, V (codes), MS, VS (scales), C
 //   pack     G = first moment, C = second moment (read), M, V, MS, VS (written)
@@ -38,7 +38,7 @@ struct AwTensor {
   unsigned index;                  // place in the caller's list (noise stream)
   unsigned first;                  // its first run among those of the table
   AwType wt, gt, ct;
-  unsigned char vec;               // every pointer aligned for the wide path
+  unsigned char vec;               // 2: every pointer is aligned to 8 elements, 1: the 8-bit codes are
 };
 
 template <int N>

@@ -85,7 +85,7 @@ class Tables {
     std::fill_n(&open_[0][0][0], 2 * 4 * 4, -1);
   }
   void add(const AwTensor& t) {
-    int& open = open_[t.vec][by_output_ ? t.ct : t.wt][t.gt];
+    int& open = open_[t.vec == 2][by_output_ ? t.ct : t.wt][t.gt];
     const long long blocks = (long long)blocks_of(t.numel);
     if (open < 0 || tabs_[open]->n == AW_MAX || blocks_[open] + blocks > MAX_BLOCKS) {
       open = (int)tabs_.size();
@@ -180,7 +180,7 @@ AwTensor step_tensor(const T& a, int i, std::vector<Range>& r) {
   t.lr_scale = a.lr_scale;
   t.wd = a.weight_decay;
   t.index = (unsigned)i;
-  t.vec = aligned(a.W, 8 * width(t.wt)) && aligned(a.G, 8 * width(t.gt)) && aligned(a.copy, 16);
+  t.vec = aligned(a.W, 8 * width(t.wt)) && aligned(a.G, 8 * width(t.gt)) && aligned(a.copy, 16) ? 2 : 1;
   return t;
 }
 
@@ -196,7 +196,7 @@ void codes(const T& a, int i, std::vector<Range>& r, AwTensor& t) {
   t.VS = a.VS;
   t.numel = a.numel;
   t.index = (unsigned)i;
-  t.vec = t.vec && aligned(a.M8, 8) && aligned(a.V8, 8);
+  if (!aligned(a.M8, 8) || !aligned(a.V8, 8)) t.vec = 0;
 }
 
 // Runs the body of an entry point: nothing is thrown across the C boundary.
@@ -281,7 +281,7 @@ std::unique_ptr<mo_list> build_adamw(const mo_adamw_tensor* list, int n) {
     buffer(l.ranges, a.V, a.numel, 4, true, "V", i);
     t.M = a.M;
     t.V = a.V;
-    t.vec = t.vec && aligned(a.M, 32) && aligned(a.V, 32);
+    if (!aligned(a.M, 32) || !aligned(a.V, 32)) t.vec = 1;
     l.tabs.add(t);
   });
 }
@@ -307,7 +307,7 @@ std::unique_ptr<mo_list> build_moments(const mo_adamw8_moments* list, int n) {
     t.W = a.M;
     t.G = a.M;
     t.C = a.V;
-    t.vec = aligned(a.M, 8 * width(a.type)) && aligned(a.V, 8 * width(a.type));
+    t.vec = aligned(a.M, 8 * width(a.type)) && aligned(a.V, 8 * width(a.type)) ? 2 : 1;
     codes(a, i, l.ranges, t);
     l.tabs.add(t);
   });
@@ -326,7 +326,7 @@ std::unique_ptr<mo_list> build_grads(const mo_grad* list, int n) {
     if (!in_place) buffer(l.ranges, a.out, a.numel, width(t.ct), true, "out", i);
     t.G = a.G;
     t.C = in_place ? const_cast<void*>(a.G) : a.out;
-    t.vec = aligned(a.G, 8 * width(t.gt)) && aligned(t.C, 8 * width(t.ct));
+    t.vec = aligned(a.G, 8 * width(t.gt)) && aligned(t.C, 8 * width(t.ct)) ? 2 : 1;
     t.numel = a.numel;
     t.index = (unsigned)i;
     l.tabs.add(t);

@@ -514,27 +514,42 @@ def test_another_stream_and_a_list_kept():
         assert torch.equal(a, b)
 
 
-def test_wide_and_narrow_paths_agree():
-    """The same numbers at an odd offset give the same bits, weights included."""
+@pytest.mark.parametrize("n", [70001, 256 * 9, 256 * 9 + 7, 256 * 9 + 8, 519, 264])
+def test_every_alignment_gives_the_same_bits(n):
+    """The same numbers at every offset from an aligned address, and with codes at an odd one, weights included."""
     import torch
     ctx = context()
-    n = 70001
     x = _inputs([n], 31)[0]
     res = []
-    for shift in (0, 1):
-        def at(a, dtype):
-            t = torch.zeros(n + 16, dtype=dtype, device="cuda")[shift:shift + n]
+    for shift in (*range(10), 100):
+        def at(a, dtype, off=shift):
+            full = torch.full((n + 64,), 3.0, device="cuda").to(dtype)
+            t = full[off % 64:off % 64 + n]
             t.copy_(torch.from_numpy(np.asarray(a)))
+            kept.append((full, off % 64))
             return t
-        W, G = at(x[0], torch.bfloat16), at(x[1], torch.bfloat16)
-        d = _state([x], shift)[0]
+        kept = []
+        W, G, C = at(x[0], torch.bfloat16), at(x[1], torch.float16, shift + 3 if shift else 0), at(x[0], torch.float16)
+        d = _state([x], 1 if shift == 100 else 0)[0]
         d = {k: d[k] for k in ("M8", "V8", "MS", "VS")}
         ctx.adamw8_step([dict(W=W, G=G, **d)], 4, seed=8)
-        W32, M, V = at(x[0], torch.float32), at(x[2], torch.float32), at(x[3], torch.float32)
-        ctx.adamw_step([dict(W=W32, G=G, M=M, V=V)], 4)
-        res.append([W, *d.values(), W32, M, V])
-    for a, b in zip(*res):
-        assert torch.equal(a, b)
+        W32, M, V = at(x[0], torch.float32, 2 * shift), at(x[2], torch.float32), at(x[3], torch.float32)
+        ctx.adamw_step([dict(W=W32, G=G, M=M, V=V, copy=C)], 4)
+        e = {k: torch.zeros_like(v) for k, v in d.items()}
+        if shift == 100:
+            e = {k: torch.zeros(v.numel() + 1, dtype=torch.uint8, device="cuda")[1:] for k, v in d.items()}
+        ctx.adamw8_pack([dict(M=M, V=V, **e)], seed=3, step=2)
+        m, v, o = at(0 * x[0], torch.bfloat16), at(0 * x[0], torch.bfloat16), at(0 * x[0], torch.float32)
+        ctx.adamw8_unpack([dict(M=m, V=v, **e)])
+        _, factor = ctx.clip_grads([dict(G=G, out=o)], 1e-3)
+        assert torch.equal(o, G.float() * factor)
+        for full, off in kept:
+            rest = torch.cat([full[:off], full[off + n:]])
+            assert bool((rest == torch.full_like(rest, 3.0)).all())
+        res.append([W, *d.values(), W32, M, V, C, *e.values(), m, v, G])
+    for r in res[1:]:
+        for a, b in zip(res[0], r):
+            assert torch.equal(a, b)
 
 
 def test_a_training_step_of_a_whole_model():
