@@ -29,12 +29,12 @@ namespace mo {
 namespace {
 
 constexpr int PER = AW_BLOCK / 32;     // elements of a lane
-// CTAs (warps) of a step on one SM: five for each of its four schedulers, at 96
-// registers.  16 and 24 take 12 and 7 % longer (8 bits), 21 as long as 24 would:
-// a scheduler with one warp more than the others finishes last.  Without two
-// buffers (shifted) 28 are best: 202 us for 54 M bf16 elements, 225 with 20.
-constexpr int STEP_CTAS = 20;
-constexpr int SHIFTED_CTAS = 28;
+// CTAs (warps) of a step on one SM, the same number for each of its four
+// schedulers (with one warp more than the others, a scheduler finishes last: 21
+// were as slow as 24 would be).  fp32 moments: 20 at 96 registers, 8 bits and
+// shifted: 28 at 72 (50 M bf16 elements: 99 us; 24: 102, 32: 105).
+constexpr int STEP32_CTAS = 20;
+constexpr int STEP8_CTAS = 28;
 
 // A lane's place in a block: wide lanes (1) and shifted ones (2) hold 8
 // neighbours, narrow ones (0) elements 32 apart.
@@ -101,6 +101,8 @@ __device__ __forceinline__ void store_words(const unsigned (&w)[4], void* p) {
 __device__ __forceinline__ void store_words(const unsigned (&w)[2], void* p) {
   asm volatile("st.global.v2.b32 [%0], {%1, %2};" ::"l"(p), "r"(w[0]), "r"(w[1]) : "memory");
 }
+
+__device__ __forceinline__ void ask_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 // Shifted accesses: 8 neighbours of a lane at an address that is aligned to its
 // elements alone.  A lane reads the 16-byte words that its elements begin in and
@@ -333,9 +335,13 @@ __device__ __forceinline__ void fetch_all(const Op& op, typename Op::Load (&in)[
   (op.template fetch<K, WIDE>(in[K], at), ...);
 }
 
-// Blocks [r, end) of a run.  With BATCH 0 a block is fetched while the one before
-// is worked on, in two buffers and two copies of the body so that nothing moves
-// between them; else BATCH blocks are fetched and then worked on.
+// Blocks [r, end) of a run, by what an Op asks for:
+//   BATCH n > 0   n blocks are fetched and then worked on
+//   BATCH 0       a block is fetched while the one before is worked on, in two
+//                 buffers and two copies of the body so that nothing moves between
+//                 them (shifted accesses need too many registers for that: as 1)
+//   AHEAD         the next block is asked into L2: fewer registers and a shorter
+//                 body than with two buffers
 template <int WIDE, typename Op>
 __device__ __forceinline__ void work_blocks(Op& op, unsigned long long first, int r, int end) {
   unsigned at = (unsigned)r * AW_BLOCK + threadIdx.x * PER;
@@ -344,7 +350,6 @@ __device__ __forceinline__ void work_blocks(Op& op, unsigned long long first, in
     at += AW_BLOCK;
     ++r;
   };
-  // two shifted buffers take more registers than a step has
   constexpr int BATCH = Op::BATCH == 0 && WIDE == 2 ? 1 : Op::BATCH;
   if constexpr (BATCH > 0) {
     while (BATCH > 1 && r + BATCH <= end) {
@@ -356,6 +361,8 @@ __device__ __forceinline__ void work_blocks(Op& op, unsigned long long first, in
     while (r < end) {
       typename Op::Load in;
       op.template fetch<0, WIDE>(in, at);
+      if constexpr (Op::AHEAD)
+        if (r + 1 < end) op.ask(at + AW_BLOCK);
       work(in);
     }
   } else if (r < end) {
@@ -756,8 +763,9 @@ __device__ __forceinline__ void moments_of(float (&m)[PER], float (&v)[PER], con
 
 template <bool EIGHT, typename WT, typename GT>
 struct StepOp {
-  static constexpr int BATCH = 0;
-  static constexpr bool BACKWARDS = false;
+  static constexpr int BATCH = EIGHT ? 1 : 0;
+  static constexpr bool AHEAD = EIGHT;
+  static constexpr bool BACKWARDS = true;        // clip_grads's norm has read the last gradients last: 620 -> 616 us
   using Load = StepLoad<EIGHT, WT, GT>;
   using Moment = typename Load::Moment;
   const AwHyper& h;
@@ -796,6 +804,12 @@ struct StepOp {
     mo::fetch<WIDE, AT>(in.w, w + at, b);
     mo::fetch<WIDE, AT>(in.m, m + at, b);
     mo::fetch<WIDE, AT>(in.v, v + at, b);
+  }
+  __device__ __forceinline__ void ask(unsigned at) const {
+    ask_l2(g + at);
+    ask_l2(w + at);
+    ask_l2(m + at);
+    ask_l2(v + at);
   }
   template <int WIDE>
   __device__ __forceinline__ void work(const Load& in, const Place<WIDE>& b, unsigned at, int r) {
@@ -855,7 +869,7 @@ __device__ __forceinline__ void StepOp<EIGHT, WT, GT>::narrow(const AwTensor& t,
 }
 
 template <bool EIGHT, typename WT, typename GT, bool VEC, int N>
-__global__ void __launch_bounds__(AW_THREADS, VEC ? STEP_CTAS : SHIFTED_CTAS)
+__global__ void __launch_bounds__(AW_THREADS, VEC && !EIGHT ? STEP32_CTAS : STEP8_CTAS)
     adamw_kernel(const __grid_constant__ AwTableOf<N> tab, const __grid_constant__ AwHyper h) {
   pdl_wait();
   pdl_trigger();
@@ -867,6 +881,7 @@ __global__ void __launch_bounds__(AW_THREADS, VEC ? STEP_CTAS : SHIFTED_CTAS)
 // ---------------------------------------------------------------- pack and unpack
 template <typename T>
 struct PackOp {
+  static constexpr bool AHEAD = false;
   static constexpr int BATCH = 2;
   static constexpr bool BACKWARDS = false;
   struct Load {
@@ -925,6 +940,7 @@ __global__ void __launch_bounds__(AW_THREADS) pack_kernel(const __grid_constant_
 
 template <typename T>
 struct UnpackOp {
+  static constexpr bool AHEAD = false;
   static constexpr int BATCH = 4;
   static constexpr bool BACKWARDS = false;
   struct Load {
@@ -988,6 +1004,7 @@ __device__ __forceinline__ double warp_sum(double x) {
 
 template <typename T>
 struct NormOp {
+  static constexpr bool AHEAD = false;
   static constexpr int BATCH = 4;
   static constexpr bool BACKWARDS = false;
   using Load = Raw<T>;
@@ -1065,6 +1082,7 @@ __global__ void __launch_bounds__(FINISH_THREADS) finish_kernel(const __grid_con
 
 template <typename T, typename OUT>
 struct ScaleOp {
+  static constexpr bool AHEAD = false;
   static constexpr int BATCH = 4;
   static constexpr bool BACKWARDS = true;
   using Load = Raw<T>;
