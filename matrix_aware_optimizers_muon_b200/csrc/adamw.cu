@@ -1,16 +1,32 @@
 // Kernels of the AdamW step over many tensors, of the 8-bit moments and of
-// gradient clipping.  All are bound by HBM traffic.
+// gradient clipping.
 //
-// A warp takes one 256-element block of a tensor, the unit that shares a scale
-// of the 8-bit moments; a lane holds 8 of its elements in registers.  On the
-// wide path (full block, aligned pointers) those are 8 neighbours, else
-// elements 32 apart, so that narrow accesses of a warp stay contiguous.
+// A CTA is one warp and works on one 256-element block of a tensor at a time, the
+// unit that shares a scale of the 8-bit moments: the scale then needs one warp
+// reduction and no shared memory, and a lane holds 8 of the elements in
+// registers.  Those are 8 neighbours, read in one access of 32, 16 or 8 bytes;
+// misaligned tensors take the aligned words around them (shifted), and blocks at
+// a tensor's ends elements 32 apart (narrow), which a warp still reads in a row.
+//
+// What bounds them, and what they reach (218 M elements, one dense layer; 6.54 TB/s
+// is the card's measured copy rate):
+//   fp32 moments, fp32 W, bf16 G and copy   28 B an element   899 us   104 % of it
+//   8-bit moments, bf16 W and G, noise      10 B              425 us    78 %
+//   unpack to bf16                           6 B              210 us    95 %
+//   pack from fp32, noise                   10 B              333 us   100 %
+//   norm of bf16 G                           2 B               65 us   102 %
+//   clip bf16 into fp32, G read twice        8 B              272 us    98 %
+// All are bound by HBM but the 8-bit step, which needs 58 instructions an element
+// with bf16 weights and noise, 14 of them for the noise, and keeps the schedulers
+// 85 % busy.
 //
 // The moments are formed in fp32 with a fixed order of roundings,
 //   m' = rn(rn(b1 m) + rn((1 - b1) g)),  v' = rn(rn(b2 v) + rn((1 - b2) rn(g g))),
 // without fused multiply-adds: the 8-bit codes are taken of these values, and
 // with 16-bit gradients b1 m + (1 - b1) g is so often a tie of two codes that
-// only a stated order makes the codes reproducible.
+// only a stated order makes the codes reproducible.  (Packed fp32x2 instructions
+// are not used for them: ptxas 12.9 joins mul.rn.f32x2 and add.rn.f32x2 into one
+// rounding, and with separate sums the step was as fast as without.)
 #include "adamw.cuh"
 
 #include <cuda_bf16.h>
@@ -110,7 +126,9 @@ __device__ __forceinline__ void ask_l2(const void* p) { asm volatile("prefetch.g
 // begin before its elements' end, with what the lane before has of them.  The
 // words at the two ends of a block hold elements of its neighbours too: a block
 // goes this way only where both neighbours (8 elements of the next) are in the
-// tensor, and those words are written by elements.
+// tensor, and those words are written by elements.  54 M elements at odd offsets:
+// 8-bit step and unpacking 199 us, element by element 307, aligned 155; clipping
+// 78, 100 and 68.
 template <int BY>
 __device__ __forceinline__ void shift_words(unsigned (&w)[8], const unsigned (&c)[12]) {
 #pragma unroll
@@ -385,9 +403,9 @@ __device__ __forceinline__ void work_blocks(Op& op, unsigned long long first, in
 //   Op::fetch<AT>(Load&, at)                   reads a whole block, AT blocks behind the lane's offset `at`
 //   Op::work(Load, Place, at, r)               works on block r of the run
 //   Op::narrow(tensor, Place, at, r)           reads and works on a partial block r, or one that has no other way
+//   Op::finish(blocks)                         the run ends
 // With VEC all tensors are aligned; without, their blocks are read shifted
 // where that is possible (t.vec), and narrow at their ends.
-//   Op::finish(blocks)                         the run ends
 template <bool VEC, int N, typename Op>
 __device__ __forceinline__ void walk(const AwTableOf<N>& tab, Op& op) {
   const unsigned lane = threadIdx.x;
@@ -473,9 +491,8 @@ struct Noise {
     for (int q = 0; q < (WIDE ? PER / 2 : PER); ++q) n.w[q] = second_word(w[q], k);
     return n;
   }
-  // Element j's 16 bits; and those with a half behind them in bits 7 to 23.
-  // (With byte permutations here nvcc 12.9 merged them with pack_tops's into
-  // wrong codes.)
+  // Element j's 16 bits; and those with a half behind them in bits 7 to 23.  By
+  // shifts and masks: where byte permutations made them, nvcc 12.9 lost v's code.
   __device__ __forceinline__ unsigned bits16(int j) const {
     return (WIDE ? j : threadIdx.x) % 2 ? w[WIDE ? j / 2 : j] >> 16 : w[WIDE ? j / 2 : j] & 0xffffu;
   }
@@ -659,8 +676,8 @@ __device__ __forceinline__ Rates rates_of(const AwHyper& h, const AwTensor& t) {
   return {rate * t.lr_scale, fmaf(-lr * t.lr_scale, t.wd, 1.f), root};
 }
 
-// sqrt and reciprocal of the hardware's special-function unit (2^-22 and
-// 2^-23 relative): the update they scale is a small part of the weight.  The
+// sqrt and reciprocal of the special-function unit (2^-23 relative each): the
+// update they scale is a small part of the weight.  The
 // forms that take subnormal numbers as zeros need two instructions, the others
 // ten; they change a denominator by less than 2^-63 / sqrt(1 - b2), which is
 // nothing beside any eps of 1e-10 or more.
@@ -882,7 +899,7 @@ __global__ void __launch_bounds__(AW_THREADS, VEC && !EIGHT ? STEP32_CTAS : STEP
 template <typename T>
 struct PackOp {
   static constexpr bool AHEAD = false;
-  static constexpr int BATCH = 2;
+  static constexpr int BATCH = 2;                // 50 M elements: 78 us; with 1 82, with two buffers 85
   static constexpr bool BACKWARDS = false;
   struct Load {
     Raw<T> m, v;
@@ -941,7 +958,7 @@ __global__ void __launch_bounds__(AW_THREADS) pack_kernel(const __grid_constant_
 template <typename T>
 struct UnpackOp {
   static constexpr bool AHEAD = false;
-  static constexpr int BATCH = 4;
+  static constexpr int BATCH = 4;                // 50 M elements: 49 us; with 8 52, with two buffers 62
   static constexpr bool BACKWARDS = false;
   struct Load {
     Raw<Code> m, v;
@@ -1005,7 +1022,7 @@ __device__ __forceinline__ double warp_sum(double x) {
 template <typename T>
 struct NormOp {
   static constexpr bool AHEAD = false;
-  static constexpr int BATCH = 4;
+  static constexpr int BATCH = 4;                // with the scaling pass, 50 M elements: 67 us; with 1 76, with 8 69
   static constexpr bool BACKWARDS = false;
   using Load = Raw<T>;
   double sum = 0.0;
@@ -1175,10 +1192,11 @@ cudaError_t launch_step(const AwTable& t, const AwHyper& h, cudaStream_t s) {
 // better than a fixed share for each of as many CTAs as fit (218 M elements:
 // fp32 step 1000 -> 905 us, 8-bit step 473 -> 454).  Long runs share the search
 // for their tensor, its rates and, with 8 bits, the sectors of the scales;
-// short ones spread a short list over the card.  65 tensors of 4096 (1040
-// blocks): 3.3 us with runs of 1, 7.7 with 8; 218 M elements, 8 bits and
-// unpacking: 1759 us with runs of 1, 685 with 4, 621 with 8; fp32: 906 with
-// 1, 903 with 2, 951 with 8.
+// short ones spread a short list over the card:
+//   65 tensors of 4096 (1040 blocks)       runs of 1: 3.3 us    8: 7.7
+//   300 odd ones, 8 bits (19 k blocks)     2: 40    4: 38       8: 48
+//   218 M elements, 8 bits, unpacking      1: 1759  4: 685      8: 622
+//   218 M elements, fp32                   1: 906   2: 903      8: 951
 int run_of(long long blocks, int most) {
   int run = 1;
   while (run < most && blocks >= 64ll * run * device_sm_count()) run *= 2;

@@ -199,17 +199,27 @@ void codes(const T& a, int i, std::vector<Range>& r, AwTensor& t) {
   if (!aligned(a.M8, 8) || !aligned(a.V8, 8)) t.vec = 0;
 }
 
+// Stores a message without throwing.
+mo_status failed(mo_ctx* ctx, mo_status st, const char* who, const char* what) noexcept {
+  try {
+    return ctx_fail(ctx, st, std::string(who) + ": " + what);
+  } catch (...) {
+    return st;
+  }
+}
+
 // Runs the body of an entry point: nothing is thrown across the C boundary.
 template <typename F>
-mo_status guarded(mo_ctx* ctx, const char* who, F body) {
+mo_status guarded(mo_ctx* ctx, const char* who, F body) noexcept {
   try {
     const cudaError_t e = body();
-    if (e != cudaSuccess) return ctx_fail(ctx, MO_ERR_CUDA, std::string(who) + ": " + cudaGetErrorString(e));
-    return MO_OK;
+    return e == cudaSuccess ? MO_OK : failed(ctx, MO_ERR_CUDA, who, cudaGetErrorString(e));
   } catch (const Refused& r) {
-    return ctx_fail(ctx, r.status, std::string(who) + ": " + r.msg);
+    return failed(ctx, r.status, who, r.msg.c_str());
   } catch (const std::exception& x) {
-    return ctx_fail(ctx, MO_ERR_UNSUPPORTED, std::string(who) + ": " + x.what());
+    return failed(ctx, MO_ERR_UNSUPPORTED, who, x.what());
+  } catch (...) {
+    return failed(ctx, MO_ERR_UNSUPPORTED, who, "unknown exception");
   }
 }
 

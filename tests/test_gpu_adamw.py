@@ -160,7 +160,8 @@ def test_adamw_types_sizes_alignment(w, g, copy, shift):
 @pytest.mark.parametrize("kw", [dict(device=True), dict(device=True, t=100000), dict(bias=False), dict(bias=False, device=True),
                                 dict(t=1, zero=True), dict(t=1, zero=True, device=True), dict(gscale=0.37),
                                 dict(w="bf16", seed=5), dict(w="bf16", seed=2 ** 63 + 11, t=70000, shift=1),
-                                dict(w="bf16", seed=0, device=True, g="bf16"), dict(t=1 << 40), dict(eps=1e-3), dict(lr=0.0)])
+                                dict(w="bf16", seed=0, device=True, g="bf16"), dict(t=1 << 40), dict(eps=1e-3), dict(lr=0.0),
+                                dict(eps=1e-12), dict(w="bf16", eps=1e-11, seed=3, shift=1), dict(gscale=0.37, shift=3, g="f16")])
 def test_adamw_options(kw):
     _adamw_case([5000, 256, 3, 2048], **kw)
 
@@ -550,6 +551,73 @@ def test_every_alignment_gives_the_same_bits(n):
     for r in res[1:]:
         for a, b in zip(res[0], r):
             assert torch.equal(a, b)
+
+
+def test_prepared_lists_are_the_calls_with_lists():
+    """A list kept over steps gives the bits of a list made for each call, with other rates, steps and gradients."""
+    import torch
+    ctx = context()
+    rng = np.random.default_rng(9)
+    sizes = [int(n) for n in rng.integers(1, 3000, 120)]             # more than a launch with few parameters takes
+    made = []
+    for _ in range(2):
+        r = np.random.default_rng(2)
+        made.append([dict(W=torch.from_numpy(r.standard_normal(n)).cuda().to(torch.bfloat16), G=torch.zeros(n, device="cuda"),
+                          weight_decay=0.1 * (i % 2)) for i, n in enumerate(sizes)])
+    for m in made:
+        for d in m:
+            d.update(ctx.adamw8_state(d["W"]))
+    kept = ctx.adamw8_tensors(made[0])
+    for t in (1, 2, 3):
+        for i, n in enumerate(sizes):
+            g = torch.from_numpy(rng.standard_normal(n)).cuda().float()
+            made[0][i]["G"].copy_(g)
+            made[1][i]["G"].copy_(g)
+        ctx.adamw8_step(kept, t, lr=1e-2 / t, seed=t)
+        ctx.adamw8_step(made[1], t, lr=1e-2 / t, seed=t)
+    for a, b in zip(*made):
+        for k in ("W", "M8", "V8", "MS", "VS"):
+            assert torch.equal(a[k], b[k])
+
+
+def test_profile_counts_the_launches():
+    import torch
+    ctx = context()
+    W = [torch.zeros(3000, device="cuda"), torch.zeros(5000, device="cuda", dtype=torch.bfloat16)]
+    mats = [dict(W=w, G=torch.ones_like(w), M=torch.zeros(w.numel(), device="cuda"), V=torch.zeros(w.numel(), device="cuda"))
+            for w in W]
+    full = [dict(M=d["M"], V=d["V"], **ctx.adamw8_state(d["M"])) for d in mats]
+    ctx.clip_grads([W[0]], 1.0)
+    ctx.profile()
+    ctx.adamw_step(mats, 1)                            # two pairs of types: two launches
+    ctx.adamw8_pack(full)
+    ctx.adamw8_unpack(full)
+    ctx.clip_grads([d["G"] for d in mats], 1.0)        # the same: norm, norm, factor, scaling, scaling
+    ctx.clip_grads([mats[0]["G"]], 1.0)                # few sums: norm, scaling
+    got = ctx.profile_read()
+    ctx.profile(False)
+    assert got["adamw"][2] == 2 and got["moments"][2] == 2 and got["clip"][2] == 7
+    assert all(got[k][0] > 0 for k in ("adamw", "moments", "clip"))
+
+
+def test_two_streams_at_once():
+    """Steps on different tensors run on two streams and need no workspace."""
+    import torch
+    ctx = context()
+    n = 1 << 20
+    x = torch.randn(n, device="cuda")
+    res = []
+    for both in (False, True):
+        sets = [[dict(W=x.clone(), G=x.clone(), M=torch.zeros(n, device="cuda"), V=torch.zeros(n, device="cuda"))] for _ in range(2)]
+        streams = [torch.cuda.Stream() for _ in range(2)] if both else [torch.cuda.current_stream()] * 2
+        torch.cuda.synchronize()
+        for t in range(1, 6):
+            for m, s in zip(sets, streams):
+                ctx.adamw_step(m, t, stream=s)
+        torch.cuda.synchronize()
+        res.append([m[0]["W"] for m in sets])
+    for w in res[1]:
+        assert torch.equal(w, res[0][0])
 
 
 def test_a_training_step_of_a_whole_model():
