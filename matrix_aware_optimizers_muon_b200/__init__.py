@@ -136,6 +136,7 @@ class Context:
         self.lib = _lib.load()
         self.device = torch.cuda.current_device() if device is None else int(device)
         self._device = torch.device("cuda", self.device)
+        self._torch = torch
         h = c_void_p()
         st = self.lib.mo_ctx_create(byref(h), self.device)
         if st != 0:
@@ -500,8 +501,11 @@ class Context:
             arr[i] = Grad(G.numel(), _addr(G), _addr(out), gt, ot)
         return self._prepare("grads", self.lib.mo_grad_list, arr, keep)
 
+    def _raw_stream(self, stream):
+        return (self._torch.cuda.current_stream(self.device) if stream is None else stream).cuda_stream
+
     def _adamw(self, fn, mats, step, lr, beta1, beta2, eps, bias_correction, grad_scale, skip, seed, stream):
-        import torch
+        torch = self._torch
         step_dev = lr_dev = None
         if isinstance(step, torch.Tensor):
             step, step_dev = 1, _scalar(step, "step", self.device, torch.int64)
@@ -510,7 +514,7 @@ class Context:
         cfg = AdamWCfg(lr, beta1, beta2, eps, bool(bias_correction), seed is not None, seed or 0, lr_dev, step_dev,
                        _scalar(grad_scale, "grad_scale", self.device, torch.float32),
                        _scalar(skip, "skip", self.device, torch.int32))
-        self._check(fn(self.handle, mats.handle, cfg, int(step), self._stream(stream)))
+        self._check(fn(self.handle, mats.handle, cfg, int(step), self._raw_stream(stream)))
 
     def adamw_step(self, mats, step, *, lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, bias_correction=True,
                    grad_scale=None, skip=None, seed=None, stream=None):
@@ -535,18 +539,18 @@ class Context:
     def adamw8_pack(self, mats, *, seed=None, step=0, stream=None):
         """Moments M, V to 8-bit codes (adamw8_moments, or what it takes); with a
         ``seed`` V is rounded stochastically, with the bits of ``step``."""
-        import torch
+        torch = self._torch
         mats = self._list("moments", mats)
         step_dev = None
         if isinstance(step, torch.Tensor):
             step, step_dev = 0, _scalar(step, "step", self.device, torch.int64)
         cfg = PackCfg(seed is not None, seed or 0, int(step), step_dev)
-        self._check(self.lib.adamw8_pack_list(self.handle, mats.handle, cfg, self._stream(stream)))
+        self._check(self.lib.adamw8_pack_list(self.handle, mats.handle, cfg, self._raw_stream(stream)))
 
     def adamw8_unpack(self, mats, *, stream=None):
         """The values that 8-bit codes stand for, written to M and V."""
         mats = self._list("moments", mats)
-        self._check(self.lib.adamw8_unpack_list(self.handle, mats.handle, self._stream(stream)))
+        self._check(self.lib.adamw8_unpack_list(self.handle, mats.handle, self._raw_stream(stream)))
 
     def clip_grads(self, grads, max_norm, *, apply=True, scale=None, nonfinite=None, stream=None, reserve=True):
         """Scales the gradients of a list (clip_tensors, or what it takes) so that
@@ -555,7 +559,7 @@ class Context:
         takes the factor as grad_scale).  ``scale`` (fp32 device scalar)
         multiplies the gradients first; ``nonfinite`` (int32 device scalar)
         receives 1 when the norm is not finite."""
-        import torch
+        torch = self._torch
         grads = self._list("grads", grads)
         if reserve and (self._workspace is None or self._workspace.numel() < _lib.CLIP_WORKSPACE_BYTES):
             self.attach_workspace(_lib.CLIP_WORKSPACE_BYTES, stream)
@@ -567,7 +571,7 @@ class Context:
         at = norm.data_ptr()
         cfg = ClipCfg(max_norm, bool(apply), _scalar(scale, "scale", self.device, torch.float32), at, at + 4,
                       _scalar(nonfinite, "nonfinite", self.device, torch.int32))
-        self._check(self.lib.clip_grads_list(self.handle, grads.handle, cfg, self._stream(stream)))
+        self._check(self.lib.clip_grads_list(self.handle, grads.handle, cfg, self._raw_stream(stream)))
         return norm, factor
 
     def gemm_bf16(self, A, B, D, *, M, N, K, batch=1, a_mn=False, b_mn=False, sym=False,
