@@ -81,7 +81,8 @@ class Tables {
  public:
   // most_run: the longest run; by_output: clip_grads leaves wt alone and
   // launches by the output's type instead
-  explicit Tables(int most_run, bool by_output = false) : most_run_(most_run), by_output_(by_output) {
+  explicit Tables(int most_run, int warps = STEP_RUNS, bool by_output = false)
+      : most_run_(most_run), warps_(warps), by_output_(by_output) {
     std::fill_n(&open_[0][0][0], 2 * 4 * 4, -1);
   }
   void add(const AwTensor& t) {
@@ -100,7 +101,7 @@ class Tables {
   void finish() {
     for (size_t k = 0; k < tabs_.size(); ++k) {
       AwTable& tab = *tabs_[k];
-      tab.run = run_of(blocks_[k], most_run_);
+      tab.run = run_of(blocks_[k], most_run_, warps_);
       tab.runs = 0;
       for (int i = 0; i < tab.n; ++i) {
         tab.t[i].first = tab.runs;
@@ -113,7 +114,7 @@ class Tables {
 
  private:
   static constexpr long long MAX_BLOCKS = 0x7fffffffll;
-  int most_run_;
+  int most_run_, warps_;
   bool by_output_;
   std::vector<std::unique_ptr<AwTable>> tabs_;
   std::vector<long long> blocks_;
@@ -324,7 +325,7 @@ std::unique_ptr<mo_list> build_moments(const mo_adamw8_moments* list, int n) {
 }
 
 std::unique_ptr<mo_list> build_grads(const mo_grad* list, int n) {
-  return build(LIST_GRADS, list, n, Tables(AW_RUN, true), [](const mo_grad& a, int i, mo_list& l) {
+  return build(LIST_GRADS, list, n, Tables(AW_RUN, GRAD_RUNS, true), [](const mo_grad& a, int i, mo_list& l) {
     if (a.G == nullptr) return;
     const bool in_place = a.out == nullptr || a.out == a.G;
     if (!type_ok(a.g_type) || (a.out != nullptr && !type_ok(a.out_type))) refuse("bad g_type or out_type" + at(i));
