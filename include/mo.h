@@ -371,8 +371,9 @@ MO_API mo_status mo_soap_muon_workspace_bytes(mo_ctx* ctx, const mo_soap_muon_ma
  *    they replace `step` and cfg->lr.  *step_dev must be >= 1.
  *  - skip: when *skip != 0 the call changes nothing (e.g. the nonfinite flag of
  *    clip_grads).
- *  - Buffers that a call writes must not overlap any other buffer of the call;
- *    such a list is refused. */
+ *  - Buffers that a call writes must not overlap any other buffer of the call,
+ *    device scalars included; such a call is refused.  A gradient may serve
+ *    several tensors. */
 typedef enum { MO_F32 = 0, MO_BF16 = 1, MO_F16 = 2 } mo_type;
 
 typedef struct {
@@ -506,7 +507,8 @@ MO_API mo_status clip_grads(mo_ctx* ctx, const mo_grad* list /* host array */, i
  * passes it to every step (the checks and tables of 300 tensors take the host
  * some 30 us, a step with a prepared list 4).  A list holds addresses and
  * sizes, in host memory, and no contents.  A moments list serves adamw8_pack
- * and adamw8_unpack.  Results and refusals are those of the calls with arrays;
+ * and adamw8_unpack (none of its buffers may overlap another, in the calls with
+ * arrays either).  Results and refusals are those of the calls with arrays;
  * *out is NULL after a refusal.  mo_list_destroy takes NULL. */
 typedef struct mo_list mo_list;
 

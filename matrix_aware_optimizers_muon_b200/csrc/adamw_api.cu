@@ -124,7 +124,7 @@ class Tables {
 bool finite_nonneg(double x) { return std::isfinite(x) && x >= 0.0; }
 
 AwHyper hyper(const mo_adamw_cfg& c, int64_t step) {
-  if (!finite_nonneg(c.lr) || !finite_nonneg(c.eps)) refuse("lr and eps must be finite and >= 0");
+  if (!finite_nonneg((float)c.lr) || !finite_nonneg((float)c.eps)) refuse("lr and eps must be finite (fp32) and >= 0");
   if (!(c.beta1 >= 0.0 && c.beta1 < 1.0) || !(c.beta2 >= 0.0 && c.beta2 < 1.0)) refuse("betas must be in [0, 1)");
   if (c.step_dev == nullptr && step < 1) refuse("step must be >= 1");
   if (!aligned(c.lr_dev, 4) || !aligned(c.step_dev, 8) || !aligned(c.grad_scale, 4) || !aligned(c.skip, 4))
@@ -271,6 +271,13 @@ bool touches(const mo_list& l, const void* p, size_t bytes) {
   return false;
 }
 
+// Whether p is in memory that the list writes (which no other range of it meets).
+bool in_written(const mo_list& l, const void* p) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+  auto x = std::upper_bound(l.ranges.begin(), l.ranges.end(), at, [](uintptr_t a, const Range& b) { return a < b.lo; });
+  return x != l.ranges.begin() && (--x)->written && at < x->hi;
+}
+
 template <typename T, typename F>
 std::unique_ptr<mo_list> build(ListKind kind, const T* list, int n, Tables tabs, F fill) {
   if (n < 0) refuse("n < 0");
@@ -358,6 +365,9 @@ const T& given(const T* cfg) {
 
 cudaError_t run_adamw(mo_ctx* ctx, const mo_list& l, const mo_adamw_cfg& cfg, int64_t step, void* stream) {
   const AwHyper h = hyper(cfg, step);
+  const void* scalars[] = {cfg.lr_dev, cfg.step_dev, cfg.grad_scale, cfg.skip};
+  for (const void* p : scalars)
+    if (in_written(l, p)) refuse("buffers overlap");
   const bool eight = l.kind == LIST_ADAMW8;
   return launch_all(ctx, l.tabs, [&](const AwTable& tab) {
     return eight ? launch_adamw8(tab, h, static_cast<cudaStream_t>(stream))
@@ -368,6 +378,7 @@ cudaError_t run_adamw(mo_ctx* ctx, const mo_list& l, const mo_adamw_cfg& cfg, in
 cudaError_t run_pack(mo_ctx* ctx, const mo_list& l, const mo_pack_cfg& cfg, void* stream) {
   AwHyper h = {};
   if (!aligned(cfg.step_dev, 8)) refuse("device scalars must be aligned to their type");
+  if (in_written(l, cfg.step_dev)) refuse("buffers overlap");
   h.stochastic = cfg.stochastic != 0;
   h.seed = cfg.seed;
   h.step = cfg.step;

@@ -56,7 +56,7 @@ def _step(lib, ctx, tensors, cfg=None, step=1):
 
 @pytest.mark.parametrize("make", [_tensor, _tensor8])
 @pytest.mark.parametrize("kw,word", [
-    (dict(lr=-1.0), "lr"), (dict(lr=float("nan")), "lr"), (dict(eps=float("inf")), "eps"), (dict(beta1=1.0), "betas"),
+    (dict(lr=-1.0), "lr"), (dict(lr=1e39), "lr"), (dict(lr=float("nan")), "lr"), (dict(eps=float("inf")), "eps"), (dict(beta1=1.0), "betas"),
     (dict(beta2=-0.1), "betas"), (dict(beta2=float("nan")), "betas"), (dict(lr_dev=18), "aligned"),
     (dict(step_dev=12), "aligned"), (dict(grad_scale=2), "aligned"), (dict(skip=1), "aligned")])
 def test_bad_hyperparameters(lib, ctx, make, kw, word):
@@ -114,6 +114,13 @@ def test_the_same_tensor_twice(lib, ctx):
     other = dict(W=8 << 20, M=9 << 20, V=10 << 20)
     st, msg = _step(lib, ctx, [_tensor(), _tensor(**other, g_type=3)])
     assert st == BAD and "g_type" in msg                   # the next fault is found, not the gradient
+
+
+def test_scalars_inside_written_buffers(lib, ctx):
+    for make, first in ((_tensor, 3 << 20), (_tensor8, 5 << 20)):
+        for kw in (dict(lr_dev=(1 << 20) + 3996), dict(step_dev=first), dict(grad_scale=4 << 20), dict(skip=1 << 20)):
+            st, msg = _step(lib, ctx, [make()], _cfg(**kw))
+            assert st == BAD and "overlap" in msg, kw
 
 
 def test_moments(lib, ctx):
