@@ -118,7 +118,11 @@ __device__ __forceinline__ void store_words(const unsigned (&w)[2], void* p) {
   asm volatile("st.global.v2.b32 [%0], {%1, %2};" ::"l"(p), "r"(w[0]), "r"(w[1]) : "memory");
 }
 
-__device__ __forceinline__ void ask_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+// Asks the block behind p's into L2.
+template <typename T>
+__device__ __forceinline__ void ask_next(const T* p) {
+  asm volatile("prefetch.global.L2 [%0 + %1];" ::"l"(p), "n"(AW_BLOCK * (int)sizeof(T)));
+}
 
 // Shifted accesses: 8 neighbours of a lane at an address that is aligned to its
 // elements alone.  A lane reads the 16-byte words that its elements begin in and
@@ -380,7 +384,7 @@ __device__ __forceinline__ void work_blocks(Op& op, unsigned long long first, in
       typename Op::Load in;
       op.template fetch<0, WIDE>(in, at);
       if constexpr (Op::AHEAD)
-        if (r + 1 < end) op.ask(at + AW_BLOCK);
+        if (r + 1 < end) op.ask(at);
       work(in);
     }
   } else if (r < end) {
@@ -823,10 +827,10 @@ struct StepOp {
     mo::fetch<WIDE, AT>(in.v, v + at, b);
   }
   __device__ __forceinline__ void ask(unsigned at) const {
-    ask_l2(g + at);
-    ask_l2(w + at);
-    ask_l2(m + at);
-    ask_l2(v + at);
+    ask_next(g + at);
+    ask_next(w + at);
+    ask_next(m + at);
+    ask_next(v + at);
   }
   template <int WIDE>
   __device__ __forceinline__ void work(const Load& in, const Place<WIDE>& b, unsigned at, int r) {
