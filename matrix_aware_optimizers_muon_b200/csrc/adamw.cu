@@ -10,13 +10,13 @@
 //
 // What bounds them, and what they reach (218 M elements, one dense layer; 6.54 TB/s
 // is the card's measured copy rate):
-//   fp32 moments, fp32 W, bf16 G and copy   28 B an element   899 us   104 % of it
-//   8-bit moments, bf16 W and G, noise      10 B              425 us    78 %
-//   unpack to bf16                           6 B              210 us    95 %
-//   pack from fp32, noise                   10 B              333 us   100 %
+//   fp32 moments, fp32 W, bf16 G and copy   28 B an element   900 us   104 % of it
+//   8-bit moments, bf16 W and G, noise      10 B              390 us    86 %
+//   unpack to bf16                           6 B              197 us   102 %
+//   pack from fp32, noise                   10 B              313 us   107 %
 //   norm of bf16 G                           2 B               65 us   102 %
-//   clip bf16 into fp32, G read twice        8 B              272 us    98 %
-// All are bound by HBM but the 8-bit step, which needs 58 instructions an element
+//   clip bf16 into fp32, G read twice        8 B              273 us    98 %
+// All are bound by HBM but the 8-bit step, which needs 57 instructions an element
 // with bf16 weights and noise, 14 of them for the noise, and keeps the schedulers
 // 85 % busy.
 //
@@ -1196,7 +1196,8 @@ cudaError_t launch_step(const AwTable& t, const AwHyper& h, cudaStream_t s) {
 // better than a fixed share for each of as many CTAs as fit (218 M elements:
 // fp32 step 1000 -> 905 us, 8-bit step 473 -> 454).  Long runs share the search
 // for their tensor, its rates and, with 8 bits, the sectors of the scales;
-// short ones spread a short list over the card:
+// short ones spread a short list over the card (of 16 they win 2 % of the 8-bit
+// step at 218 M elements and lose 1 to 15 % below 80 M):
 //   65 tensors of 4096 (1040 blocks)       runs of 1: 3.3 us    8: 7.7
 //   300 odd ones, 8 bits (19 k blocks)     2: 40    4: 38       8: 48
 //   218 M elements, 8 bits, unpacking      1: 1759  4: 685      8: 622
