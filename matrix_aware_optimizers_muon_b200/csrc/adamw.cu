@@ -128,9 +128,10 @@ __device__ __forceinline__ void ask_next(const T* p) {
 // elements alone.  A lane reads the 16-byte words that its elements begin in and
 // the one behind, which L1 holds for the next lane; it writes the words that
 // begin before its elements' end, with what the lane before has of them.  The
-// words at the two ends of a block hold elements of its neighbours too: a block
-// goes this way only where both neighbours (8 elements of the next) are in the
-// tensor, and those words are written by elements.  54 M elements at odd offsets:
+// words at the two ends of a block hold elements of its neighbours too, so those
+// are written by elements.  What is read before a tensor's first element is in
+// the same 16 bytes and so in the same allocation; behind its last one that need
+// not be, so a block goes this way only where 8 elements of the tensor follow it.  54 M elements at odd offsets:
 // 8-bit step and unpacking 199 us, element by element 307, aligned 155; clipping
 // 78, 100 and 68.
 template <int BY>
@@ -357,7 +358,7 @@ __device__ __forceinline__ void fetch_all(const Op& op, typename Op::Load (&in)[
   (op.template fetch<K, WIDE>(in[K], at), ...);
 }
 
-// Blocks [r, end) of a run, by what an Op asks for:
+// The first `end` blocks of a run, by what an Op asks for:
 //   BATCH n > 0   n blocks are fetched and then worked on
 //   BATCH 0       a block is fetched while the one before is worked on, in two
 //                 buffers and two copies of the body so that nothing moves between
@@ -365,8 +366,9 @@ __device__ __forceinline__ void fetch_all(const Op& op, typename Op::Load (&in)[
 //   AHEAD         the next block is asked into L2: fewer registers and a shorter
 //                 body than with two buffers
 template <int WIDE, typename Op>
-__device__ __forceinline__ void work_blocks(Op& op, unsigned long long first, int r, int end) {
-  unsigned at = (unsigned)r * AW_BLOCK + threadIdx.x * PER;
+__device__ __forceinline__ void work_blocks(Op& op, unsigned long long first, int end) {
+  unsigned at = threadIdx.x * PER;
+  int r = 0;
   const auto work = [&](const typename Op::Load& in) {
     op.work(in, Place<WIDE>{first + at, 0}, at, r);
     at += AW_BLOCK;
@@ -421,19 +423,13 @@ __device__ __forceinline__ void walk(const AwTableOf<N>& tab, Op& op) {
     const long long block = (long long)(run - t.first) * tab.run;
     const unsigned long long first = (unsigned long long)block * AW_BLOCK;
     const int blocks = (int)min((long long)tab.run, (t.numel + AW_BLOCK - 1) / AW_BLOCK - block);
-    // blocks [from, to) are whole (VEC), or have both neighbours: the tensor's first has none before it
-    int from = 0, to = 0;
-    if (VEC) {
-      to = (int)min((long long)blocks, t.numel / AW_BLOCK - block);
-    } else if (t.vec) {
-      from = block == 0 ? 1 : 0;
-      to = (int)max((long long)from, min((long long)blocks, (t.numel - 8) / AW_BLOCK - block));
-    }
+    // the whole blocks (VEC), or those with 8 elements behind them
+    int whole = 0;
+    if (VEC) whole = (int)min((long long)blocks, t.numel / AW_BLOCK - block);
+    else if (t.vec) whole = (int)max(0ll, min((long long)blocks, (t.numel - 8) / AW_BLOCK - block));
     op.start(t, first, blocks);
-    work_blocks<VEC ? 1 : 2>(op, first, from, to);
-    for (int r = 0; r < blocks; ++r) {
-      if (r == from) r = to;
-      if (r >= blocks) break;
+    work_blocks<VEC ? 1 : 2>(op, first, whole);
+    for (int r = whole; r < blocks; ++r) {
       const unsigned at = (unsigned)r * AW_BLOCK + lane;
       const long long left = t.numel - (long long)(first + at);
       op.narrow(t, Place<0>{first + at, left < AW_BLOCK ? (int)left : AW_BLOCK}, at, r);
@@ -809,10 +805,10 @@ struct StepOp {
     m = static_cast<Moment*>(t.M) + first;
     v = static_cast<Moment*>(t.V) + first;
     c = static_cast<unsigned short*>(t.C) + first;
-    s.start(h, t);
   }
   __device__ __forceinline__ void start(const AwTensor& t, unsigned long long first, int blocks) {
     point(t, first);
+    s.start(h, t);
     if (EIGHT) {
       ms = t.MS + first / AW_BLOCK;
       vs = t.VS + first / AW_BLOCK;
@@ -875,10 +871,11 @@ struct StepOp {
 // A narrow block, apart from the registers of the main path; returns the run's
 // scales.
 template <bool EIGHT, typename WT, typename GT>
-__device__ __noinline__ unsigned step_tail(const AwTensor& t, const AwHyper& h, float gs, unsigned long long first, int left,
-                                           unsigned scales, int r) {
+__device__ __noinline__ unsigned step_tail(const AwTensor& t, const AwHyper& h, float gs, Shared s, unsigned long long first,
+                                           int left, unsigned scales, int r) {
   StepOp<EIGHT, WT, GT> op(h, gs);
   op.point(t, first - threadIdx.x);
+  op.s = s;
   op.scales.all = scales;
   op.work_narrow(Place<0>{first, left}, threadIdx.x, r);
   return op.scales.all;
@@ -886,7 +883,7 @@ __device__ __noinline__ unsigned step_tail(const AwTensor& t, const AwHyper& h, 
 
 template <bool EIGHT, typename WT, typename GT>
 __device__ __forceinline__ void StepOp<EIGHT, WT, GT>::narrow(const AwTensor& t, const Place<0>& b, unsigned, int r) {
-  scales.all = step_tail<EIGHT, WT, GT>(t, h, gs, b.first, b.left, EIGHT ? scales.all : 0, r);
+  scales.all = step_tail<EIGHT, WT, GT>(t, h, gs, s, b.first, b.left, EIGHT ? scales.all : 0, r);
 }
 
 template <bool EIGHT, typename WT, typename GT, bool VEC, int N>
