@@ -506,7 +506,8 @@ struct Noise {
 // A block of 256 elements shares one scale 2^(s - 127) for each moment, a
 // power of two taken from the exponent field E of its largest magnitude, so
 // that scaling is exact and a code of an unchanged block stays what it is.
-//   m: e4m3, s = max(1, E - 7), nearest-even.
+//   m: e4m3, s = max(1, E - 7), nearest-even: a step moves m by a tenth of
+//      g - m, with g's own scatter, so that it does not stick to a code.
 //   v: exponent and mantissa of a float with 5 and 3 bits and no sign,
 //      s = max(1, E - 15).  Its range 2^33 is about the square of e4m3's 2^17,
 //      as v is of m.  Nearest-even, or stochastic: (1 - b2) (g^2 - v) is far

@@ -600,6 +600,34 @@ def test_profile_counts_the_launches():
     assert all(got[k][0] > 0 for k in ("adamw", "moments", "clip"))
 
 
+@pytest.mark.parametrize("shift", [0, 1, 5])
+def test_steps_in_a_row(shift):
+    """Twenty steps that nothing waits between give the bits of twenty with a wait after each: a step's words around a
+    block are not seen again by the next step."""
+    import torch
+    ctx = context()
+    sizes = [300007, 1000, 70001]
+    res = []
+    for wait in (True, False):
+        arrays = _inputs(sizes, 13)
+        W, G = Flat([a[0] for a in arrays], torch.bfloat16, shift), Flat([a[1] for a in arrays], torch.bfloat16, shift)
+        W32, M, V = (Flat([a[k] for a in arrays], torch.float32, shift) for k in (0, 2, 3))
+        st = _state(arrays, 0)
+        l8 = ctx.adamw8_tensors([dict(W=w, G=g, **{k: d[k] for k in ("M8", "V8", "MS", "VS")})
+                                 for w, g, d in zip(W.views, G.views, st)])
+        l32 = ctx.adamw_tensors([dict(W=w, G=g, M=m, V=v) for w, g, m, v in zip(W32.views, G.views, M.views, V.views)])
+        torch.cuda.synchronize()
+        for t in range(1, 21):
+            ctx.adamw8_step(l8, t, lr=1e-2, seed=1)
+            ctx.adamw_step(l32, t, lr=1e-2)
+            if wait:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        res.append([W.buf, W32.buf, M.buf, V.buf, *(d[k] for d in st for k in ("M8", "V8", "MS", "VS"))])
+    for a, b in zip(*res):
+        assert torch.equal(a, b)
+
+
 def test_two_streams_at_once():
     """Steps on different tensors run on two streams and need no workspace."""
     import torch
