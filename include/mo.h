@@ -391,7 +391,9 @@ typedef struct {
 typedef struct {
   double lr, beta1, beta2, eps;    /* lr >= 0, 0 <= beta < 1, eps >= 0 */
   int bias_correction;             /* 1: divide by 1 - beta^t (default) */
-  int stochastic;                  /* 1: stochastic rounding (bf16 W, 8-bit V) */
+  int stochastic;                  /* 1: stochastic rounding (bf16 W, both 8-bit
+                                      moments); 2: the same, 8-bit M to nearest
+                                      (see adamw8_step); 0: to nearest */
   uint64_t seed;
   const float* lr_dev;             /* optional device scalars */
   const int64_t* step_dev;
@@ -413,11 +415,18 @@ MO_API mo_status adamw_step(mo_ctx* ctx, const mo_adamw_tensor* list /* host arr
  * with E the biased exponent of the block's largest finite fp32 magnitude.  The
  * scales are powers of two, so the codes of an unchanged block stay what they
  * are.  An infinite first moment becomes a NaN, which e4m3 has.  W is computed
- * from the new moments before they are rounded to codes.  M is rounded to
- * nearest-even; V to nearest-even or, with stochastic != 0, up with the
- * probability of its distance: with b2 = 0.999 V moves by 0.1 % of itself in a
- * step and half a step of its code is 3 to 6 %, so that nearest rounding would
- * leave a slowly changing V where it is.  All zero codes and scales are the
+ * from the new moments before they are rounded to codes.
+ * With stochastic == 1 both moments take the code above (in magnitude) with the
+ * probability of their distance from the one below, from bits that are a function
+ * of (seed, step, place in the list, element): their means follow the recurrence.
+ * Nearest-even rounding leaves a moment that changes by less than half a code step, 3
+ * to 6 % of it, where it is.  V moves by 0.1 % in a step with b2 = 0.999, M by
+ * (1 - b1) (g - M): without a gradient and with b1 = 0.95 an M of 9 or 10 eighths of
+ * its binade never decays, with b1 = 0.9 the lowest four codes never do, and
+ * with a steady one M stops at 0.5 to 0.8 of it.  So do not train with
+ * stochastic == 0 (both moments to nearest) for longer than a few steps, nor with 2 (M to
+ * nearest, V with noise: M / sqrt(V) grows without bound and W with it), which
+ * is there for runs that were begun with it and have to keep their bits.  All zero codes and scales are the
  * zero moments of the first step.  M8 and V8 hold numel bytes, MS and VS
  * ceil(numel / 256).  Everything else is as in adamw_step. */
 typedef struct {
@@ -439,7 +448,8 @@ MO_API mo_status adamw8_step(mo_ctx* ctx, const mo_adamw8_tensor* list /* host a
 
 /* Conversion between moments in fp32 or bf16 and 8 bits (checkpoints, a run
  * that changes its kind of state).  pack writes the codes of M and V, rounded
- * as adamw8_step does; a negative V takes code 0.  unpack writes the values
+ * as adamw8_step does (one conversion to nearest is as good as one with noise); a
+ * negative V takes code 0.  unpack writes the values
  * that codes stand for, exact in fp32 and in bf16 down to their subnormals. */
 typedef struct {
   int64_t numel;
@@ -453,7 +463,7 @@ typedef struct {
 } mo_adamw8_moments;
 
 typedef struct {
-  int stochastic;       /* of V, from (seed, step, place in the list, element) */
+  int stochastic;       /* as in mo_adamw_cfg: 1 both by noise, 2 V alone */
   uint64_t seed;
   int64_t step;
   const int64_t* step_dev;   /* optional; replaces step */

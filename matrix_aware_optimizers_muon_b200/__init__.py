@@ -9,6 +9,7 @@ binding's entry points fails.
 """
 
 import ctypes
+import warnings
 from ctypes import byref, c_int32, c_int64, c_size_t, c_void_p
 
 from . import _lib
@@ -107,6 +108,9 @@ def _scalar(t, name, device, dtype):
     return t.data_ptr()
 
 
+_NOT_GIVEN = object()
+
+
 class TensorList:
     """A prepared list for adamw_step, adamw8_step, adamw8_pack / adamw8_unpack or clip_grads.
 
@@ -130,6 +134,8 @@ class TensorList:
 
 class Context:
     """One library context on one CUDA device, with a torch-owned workspace."""
+
+    _warned = False         # of adamw8_step(seed=...), once
 
     def __init__(self, device=None):
         import torch
@@ -504,14 +510,14 @@ class Context:
     def _raw_stream(self, stream):
         return (self._torch.cuda.current_stream(self.device) if stream is None else stream).cuda_stream
 
-    def _adamw(self, fn, mats, step, lr, beta1, beta2, eps, bias_correction, grad_scale, skip, seed, stream):
+    def _adamw(self, fn, mats, step, lr, beta1, beta2, eps, bias_correction, grad_scale, skip, stochastic, seed, stream):
         torch = self._torch
         step_dev = lr_dev = None
         if isinstance(step, torch.Tensor):
             step, step_dev = 1, _scalar(step, "step", self.device, torch.int64)
         if isinstance(lr, torch.Tensor):
             lr, lr_dev = 0.0, _scalar(lr, "lr", self.device, torch.float32)
-        cfg = AdamWCfg(lr, beta1, beta2, eps, bool(bias_correction), seed is not None, seed or 0, lr_dev, step_dev,
+        cfg = AdamWCfg(lr, beta1, beta2, eps, bool(bias_correction), stochastic, seed or 0, lr_dev, step_dev,
                        _scalar(grad_scale, "grad_scale", self.device, torch.float32),
                        _scalar(skip, "skip", self.device, torch.int32))
         self._check(fn(self.handle, mats.handle, cfg, int(step), self._raw_stream(stream)))
@@ -525,26 +531,47 @@ class Context:
         gradient, a nonzero ``skip`` (int32) leaves everything as it is.  With a
         ``seed`` bf16 weights are rounded stochastically, else to nearest."""
         self._adamw(self.lib.adamw_step_list, self._list("adamw", mats), step, lr, beta1, beta2, eps,
-                    bias_correction, grad_scale, skip, seed, stream)
+                    bias_correction, grad_scale, skip, seed is not None, seed, stream)
+
+    @staticmethod
+    def _rounding(noise, default, seed):
+        """The library's kind of rounding of an 8-bit call, and its seed."""
+        if seed is not _NOT_GIVEN and noise != default:
+            raise ValueError("noise and seed are two kinds of rounding: give one of them")
+        if seed is _NOT_GIVEN:
+            return int(noise is not None), noise
+        return 2 * (seed is not None), seed
 
     def adamw8_step(self, mats, step, *, lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, bias_correction=True,
-                    grad_scale=None, skip=None, seed=0, stream=None):
+                    grad_scale=None, skip=None, noise=0, seed=_NOT_GIVEN, stream=None):
         """One AdamW step with both moments in 8 bits (adamw8_tensors, or what
-        it takes).  With a ``seed`` the second moment and bf16 weights are
-        rounded stochastically; None rounds to nearest, which leaves a slowly
-        changing second moment where it is.  The rest is as in adamw_step."""
-        self._adamw(self.lib.adamw8_step_list, self._list("adamw8", mats), step, lr, beta1, beta2, eps,
-                    bias_correction, grad_scale, skip, seed, stream)
+        it takes).  ``noise`` is the seed with which both moments and bf16 weights
+        are rounded stochastically; None rounds to nearest, which leaves moments
+        that change by less than half a code step where they are: over more than
+        a few steps the first no longer follows the gradient.
 
-    def adamw8_pack(self, mats, *, seed=None, step=0, stream=None):
-        """Moments M, V to 8-bit codes (adamw8_moments, or what it takes); with a
-        ``seed`` V is rounded stochastically, with the bits of ``step``."""
+        ``seed`` in place of ``noise`` is an earlier form, for runs that have to
+        keep its bits: the first moment is rounded to nearest and sticks to its code
+        while the second decays, so that weights without gradient run away."""
+        stochastic, seed = self._rounding(noise, 0, seed)
+        if stochastic == 2 and not Context._warned:
+            Context._warned = True
+            warnings.warn("adamw8_step(seed=...) rounds the first moment to the nearest code, where it sticks: "
+                          "train with noise=...", stacklevel=2)
+        self._adamw(self.lib.adamw8_step_list, self._list("adamw8", mats), step, lr, beta1, beta2, eps,
+                    bias_correction, grad_scale, skip, stochastic, seed, stream)
+
+    def adamw8_pack(self, mats, *, noise=None, seed=None, step=0, stream=None):
+        """Moments M, V to 8-bit codes (adamw8_moments, or what it takes); with
+        ``noise`` both are rounded stochastically, with ``seed`` V alone, with the bits
+        of ``step``."""
         torch = self._torch
+        stochastic, seed = self._rounding(noise, None, _NOT_GIVEN if seed is None else seed)
         mats = self._list("moments", mats)
         step_dev = None
         if isinstance(step, torch.Tensor):
             step, step_dev = 0, _scalar(step, "step", self.device, torch.int64)
-        cfg = PackCfg(seed is not None, seed or 0, int(step), step_dev)
+        cfg = PackCfg(stochastic, seed or 0, int(step), step_dev)
         self._check(self.lib.adamw8_pack_list(self.handle, mats.handle, cfg, self._raw_stream(stream)))
 
     def adamw8_unpack(self, mats, *, stream=None):

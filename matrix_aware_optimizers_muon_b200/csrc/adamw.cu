@@ -442,8 +442,9 @@ __device__ __forceinline__ void walk(const AwTableOf<N>& tab, Op& op) {
 // Bits for stochastic rounding: a function of (seed, step, place in the
 // list, element), the same whatever the launch looks like.  A tensor's two
 // 32-bit keys come from a 64-bit mix of the first three; each pair of
-// neighbours takes two 32-bit words, 16 bits of each for an element: the
-// first for its second moment, the second for a bf16 weight.
+// neighbours takes three 32-bit words, 16 bits of each for an element: the
+// first for its second moment, the second for a bf16 weight, the third for its
+// first moment.
 struct Keys {
   unsigned k1, k2;
 };
@@ -475,6 +476,11 @@ __device__ __forceinline__ unsigned second_word(unsigned first, Keys k) {
   return y ^ (y >> 16);
 }
 
+__device__ __forceinline__ unsigned third_word(unsigned first, Keys k) {
+  const unsigned z = (first ^ k.k2) * 0x9E3779B9u + k.k1;
+  return z ^ (z >> 16);
+}
+
 // The first words that a lane's elements need: wide lanes hold whole pairs,
 // narrow ones an element of each.
 template <int WIDE>
@@ -489,6 +495,12 @@ struct Noise {
     Noise n;
 #pragma unroll
     for (int q = 0; q < (WIDE ? PER / 2 : PER); ++q) n.w[q] = second_word(w[q], k);
+    return n;
+  }
+  __device__ __forceinline__ Noise third(Keys k) const {
+    Noise n;
+#pragma unroll
+    for (int q = 0; q < (WIDE ? PER / 2 : PER); ++q) n.w[q] = third_word(w[q], k);
     return n;
   }
   // Element j's 16 bits; and those with a half behind them in bits 7 to 23.  By
@@ -506,8 +518,10 @@ struct Noise {
 // A block of 256 elements shares one scale 2^(s - 127) for each moment, a
 // power of two taken from the exponent field E of its largest magnitude, so
 // that scaling is exact and a code of an unchanged block stays what it is.
-//   m: e4m3, s = max(1, E - 7), nearest-even: a step moves m by a tenth of
-//      g - m, with g's own scatter, so that it does not stick to a code.
+//   m: e4m3, s = max(1, E - 7).  Nearest-even, or stochastic (FIRST): a code step
+//      is 6 to 12 % of m, and a step moves m by (1 - b1) (g - m).  Without a
+//      gradient and with b1 = 0.95 the nearest code of 9 and 10 eighths is again 9
+//      and 10: m stays for ever, v goes on sinking and the weights run away.
 //   v: exponent and mantissa of a float with 5 and 3 bits and no sign,
 //      s = max(1, E - 15).  Its range 2^33 is about the square of e4m3's 2^17,
 //      as v is of m.  Nearest-even, or stochastic: (1 - b2) (g^2 - v) is far
@@ -515,9 +529,14 @@ struct Noise {
 //      where it is.  v > 0 never gets code 0, which would leave eps alone in
 //      the denominator; code 255 stands for a value that is not finite.
 // An fp32 value times 2^(127 - s) 2^-112 has v's code in bits 20 to 27, its
-// subnormals included, and what is rounded off below them.
+// subnormals included, and what is rounded off below them; times
+// 2^(127 - s) 2^-120 it has m's in bits 20 to 26, below its sign.  Noise is added
+// there (16 bits and a half behind them), which is unbiased to 2^-17 of a code step.
+// m's noise costs the step of 50 M elements 11 us with bf16 weights (108; v's alone
+// 98, none 87) and nothing with fp32 ones (114), where HBM is the bound.
 constexpr unsigned INF_BITS = 0x7f800000u;
 constexpr unsigned HIGH_BITS = 0x4e000000u;   // 2^29: below, v's scale is at most 2^14
+constexpr unsigned FIRST_HIGH_BITS = 0x46000000u;   // 2^13: below, m's scale is at most 2^5
 
 // 2^(s - 127) of a scale byte; 2^-127 is subnormal
 __device__ __forceinline__ float scale_of(unsigned s) { return __uint_as_float(s ? s << 23 : 0x00400000u); }
@@ -600,9 +619,29 @@ __device__ __forceinline__ void second_codes(unsigned (&r)[PER], const float (&v
   }
 }
 
+// Stochastic codes of m in bits 24 to 31 of r; mi is 2^(127 - s) 2^-120 of what m
+// is in.  What falls below the last bit of a subnormal product is cut off: the noise is a
+// whole number of these bits, so that it decides nothing.
 template <int WIDE>
+__device__ __forceinline__ void first_codes(unsigned (&r)[PER], const float (&m)[PER], float mi, const Noise<WIDE>& n) {
+  unsigned any = 0;
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    const unsigned u = __float_as_uint(__fmul_rz(m[j], mi));
+    any |= u;
+    r[j] = (u * 16u + n.bits24(j)) | (u & 0x80000000u);
+  }
+  if (rare((any & 0x78000000u) != 0)) {                // numbers stay below 2^-112 here
+#pragma unroll
+    for (int j = 0; j < PER; ++j)
+      if (!(fabsf(m[j]) < __uint_as_float(INF_BITS))) r[j] = 127u << 24;
+  }
+}
+
+// FIRST: both moments by noise; else m to nearest and v as `stochastic` says.
+template <bool FIRST, int WIDE>
 __device__ __forceinline__ void store_moments(float (&m)[PER], float (&v)[PER], Code* mp, Code* vp, Scales& scales, int r,
-                                              const Place<WIDE>& b, bool stochastic, const Noise<WIDE>& n) {
+                                              const Place<WIDE>& b, bool stochastic, const Noise<WIDE>& n, Keys k) {
   float bm = 0.f;
   unsigned bv = 0;
 #pragma unroll
@@ -615,8 +654,10 @@ __device__ __forceinline__ void store_moments(float (&m)[PER], float (&v)[PER], 
   unsigned odd = 0;                                    // elements whose v has code 255
   float scaled[PER];
   unsigned ms, vs;
-  if (!rare(um >= INF_BITS || uv >= HIGH_BITS)) {
+  float mi;                                            // FIRST: 2^(127 - s) 2^-120, a normal number below FIRST_HIGH_BITS
+  if (!rare(um >= (FIRST ? FIRST_HIGH_BITS : INF_BITS) || uv >= HIGH_BITS)) {
     ms = max(1, (int)(um >> 23) - 7);
+    mi = __uint_as_float(((FIRST ? 134u : 254u) - ms) << 23);
     vs = max(1, (int)(uv >> 23) - 15);
     const float vi = __uint_as_float((142u - vs) << 23);   // 2^(127 - s) 2^-112, a normal number below HIGH_BITS
 #pragma unroll
@@ -638,20 +679,34 @@ __device__ __forceinline__ void store_moments(float (&m)[PER], float (&v)[PER], 
     vs = max(1, (int)(uv >> 23) - 15);
 #pragma unroll
     for (int j = 0; j < PER; ++j) scaled[j] = v[j] * __uint_as_float((254u - vs) << 23) * 0x1p-112f;
+    mi = __uint_as_float((254u - ms) << 23);
+    if constexpr (FIRST) {
+      scale_all(m, mi);
+      mi = 0x1p-120f;
+    }
   }
-  scale_all(m, __uint_as_float((254u - ms) << 23));
-  unsigned mw[PER / 2], vr[PER];
+  unsigned mw[PER / 4], vr[PER];                       // four codes of m to a word
+  if constexpr (FIRST) {
+    unsigned mr[PER];
+    first_codes(mr, m, mi, n.third(k));
 #pragma unroll
-  for (int q = 0; q < PER / 2; ++q)
-    mw[q] = __nv_cvt_float2_to_fp8x2(make_float2(m[2 * q], m[2 * q + 1]), __NV_SATFINITE, __NV_E4M3);
-  if (stochastic) second_codes<true>(vr, v, scaled, n);
+    for (int q = 0; q < PER / 4; ++q) mw[q] = pack_tops(mr[4 * q], mr[4 * q + 1], mr[4 * q + 2], mr[4 * q + 3]);
+  } else {
+    scale_all(m, mi);
+    const auto pair = [&](int j) {
+      return (unsigned)__nv_cvt_float2_to_fp8x2(make_float2(m[j], m[j + 1]), __NV_SATFINITE, __NV_E4M3);
+    };
+#pragma unroll
+    for (int q = 0; q < PER / 4; ++q) mw[q] = __byte_perm(pair(4 * q), pair(4 * q + 2), 0x5410);
+  }
+  if (FIRST || stochastic) second_codes<true>(vr, v, scaled, n);
   else second_codes<false>(vr, v, scaled, n);
   if (rare(odd != 0)) {
 #pragma unroll
     for (int j = 0; j < PER; ++j)
       if (odd & (1u << j)) vr[j] = 255u << 24;
   }
-  put(Raw<Code>{{__byte_perm(mw[0], mw[1], 0x5410), __byte_perm(mw[2], mw[3], 0x5410)}, {}}, mp, b);
+  put(Raw<Code>{{mw[0], mw[1]}, {}}, mp, b);
   put(Raw<Code>{{pack_tops(vr[0], vr[1], vr[2], vr[3]), pack_tops(vr[4], vr[5], vr[6], vr[7])}, {}}, vp, b);
   scales.set(r, ms, vs);
 }
@@ -779,7 +834,7 @@ __device__ __forceinline__ void moments_of(float (&m)[PER], float (&v)[PER], con
   }
 }
 
-template <bool EIGHT, typename WT, typename GT>
+template <bool EIGHT, bool FIRST, typename WT, typename GT>
 struct StepOp {
   static constexpr int BATCH = EIGHT ? 1 : 0;
   static constexpr bool AHEAD = EIGHT;
@@ -840,9 +895,10 @@ struct StepOp {
     update(w1, m1, v1, g1, h, s.r, sm, sv);
     constexpr bool LOW = sizeof(WT) == 2;
     Noise<WIDE> n;
-    if ((EIGHT || LOW) && h.stochastic) n.draw(b, s.k);
+    const bool noisy = FIRST || h.stochastic;
+    if ((EIGHT || LOW) && noisy) n.draw(b, s.k);
     if constexpr (EIGHT) {
-      store_moments(m1, v1, m + at, v + at, scales, r, b, h.stochastic != 0, n);
+      store_moments<FIRST>(m1, v1, m + at, v + at, scales, r, b, noisy, n, s.k);
     } else {
       store(m1, m + at, b);
       store(v1, v + at, b);
@@ -851,7 +907,7 @@ struct StepOp {
     if (!LOW && s.ct == AW_F16) store(w1, reinterpret_cast<__half*>(c) + at, b);
     if constexpr (LOW) {
       Raw<WT> out;
-      if (h.stochastic) round_weights(out, w1, n.second(s.k));
+      if (noisy) round_weights(out, w1, n.second(s.k));
       else narrow_all(out, w1);
       put(out, w + at, b);
     } else {
@@ -871,10 +927,10 @@ struct StepOp {
 
 // A narrow block, apart from the registers of the main path; returns the run's
 // scales.
-template <bool EIGHT, typename WT, typename GT>
+template <bool EIGHT, bool FIRST, typename WT, typename GT>
 __device__ __noinline__ unsigned step_tail(const AwTensor& t, const AwHyper& h, float gs, Shared s, unsigned long long first,
                                            int left, unsigned scales, int r) {
-  StepOp<EIGHT, WT, GT> op(h, gs);
+  StepOp<EIGHT, FIRST, WT, GT> op(h, gs);
   op.point(t, first - threadIdx.x);
   op.s = s;
   op.scales.all = scales;
@@ -882,23 +938,23 @@ __device__ __noinline__ unsigned step_tail(const AwTensor& t, const AwHyper& h, 
   return op.scales.all;
 }
 
-template <bool EIGHT, typename WT, typename GT>
-__device__ __forceinline__ void StepOp<EIGHT, WT, GT>::narrow(const AwTensor& t, const Place<0>& b, unsigned, int r) {
-  scales.all = step_tail<EIGHT, WT, GT>(t, h, gs, s, b.first, b.left, EIGHT ? scales.all : 0, r);
+template <bool EIGHT, bool FIRST, typename WT, typename GT>
+__device__ __forceinline__ void StepOp<EIGHT, FIRST, WT, GT>::narrow(const AwTensor& t, const Place<0>& b, unsigned, int r) {
+  scales.all = step_tail<EIGHT, FIRST, WT, GT>(t, h, gs, s, b.first, b.left, EIGHT ? scales.all : 0, r);
 }
 
-template <bool EIGHT, typename WT, typename GT, bool VEC, int N>
+template <bool EIGHT, bool FIRST, typename WT, typename GT, bool VEC, int N>
 __global__ void __launch_bounds__(AW_THREADS, VEC && !EIGHT ? STEP32_CTAS : STEP8_CTAS)
     adamw_kernel(const __grid_constant__ AwTableOf<N> tab, const __grid_constant__ AwHyper h) {
   pdl_wait();
   pdl_trigger();
   if (h.skip != nullptr && *h.skip != 0) return;
-  StepOp<EIGHT, WT, GT> op(h, h.gscale ? *h.gscale : 1.f);
+  StepOp<EIGHT, FIRST, WT, GT> op(h, h.gscale ? *h.gscale : 1.f);
   walk<VEC>(tab, op);
 }
 
 // ---------------------------------------------------------------- pack and unpack
-template <typename T>
+template <bool FIRST, typename T>
 struct PackOp {
   static constexpr bool AHEAD = false;
   static constexpr int BATCH = 2;                // 50 M elements: 78 us; with 1 82, with two buffers 85
@@ -937,8 +993,9 @@ struct PackOp {
     widen_all(x, settled<WIDE>(in.m, m + at));
     widen_all(y, settled<WIDE>(in.v, v + at));
     Noise<WIDE> n;
-    if (h.stochastic) n.draw(b, k);
-    store_moments(x, y, m8 + at, v8 + at, scales, r, b, h.stochastic != 0, n);
+    const bool noisy = FIRST || h.stochastic;
+    if (noisy) n.draw(b, k);
+    store_moments<FIRST>(x, y, m8 + at, v8 + at, scales, r, b, noisy, n, k);
   }
   __device__ __forceinline__ void narrow(const AwTensor&, const Place<0>& b, unsigned at, int r) {
     Load in;
@@ -948,12 +1005,12 @@ struct PackOp {
   __device__ __forceinline__ void finish(int blocks) const { scales.store(ms, vs, blocks); }
 };
 
-template <typename T, bool VEC, int N>
+template <bool FIRST, typename T, bool VEC, int N>
 __global__ void __launch_bounds__(AW_THREADS) pack_kernel(const __grid_constant__ AwTableOf<N> tab,
                                                           const __grid_constant__ AwHyper h) {
   pdl_wait();
   pdl_trigger();
-  PackOp<T> op(h);
+  PackOp<FIRST, T> op(h);
   walk<VEC>(tab, op);
 }
 
@@ -1176,13 +1233,13 @@ cudaError_t launch_list(const void* (&forms)[2][2], int kind, const AwTable& t, 
   {{(const void*)KERNEL<__VA_ARGS__, false, AW_SHORT>, (const void*)KERNEL<__VA_ARGS__, false, AW_MAX>},            \
    {(const void*)KERNEL<__VA_ARGS__, true, AW_SHORT>, (const void*)KERNEL<__VA_ARGS__, true, AW_MAX>}}
 
-template <bool EIGHT>
+template <bool EIGHT, bool FIRST>
 cudaError_t launch_step(const AwTable& t, const AwHyper& h, cudaStream_t s) {
   return with_wide_type(t.t[0].wt, [&](auto* w) {
     return with_type(t.t[0].gt, [&](auto* g) {
       using W = Pointee<decltype(w)>;
       using G = Pointee<decltype(g)>;
-      const void* forms[2][2] = MO_FORMS(adamw_kernel, EIGHT, W, G);
+      const void* forms[2][2] = MO_FORMS(adamw_kernel, EIGHT, FIRST, W, G);
       return launch_list(forms, PK_ADAMW, t, t.runs, h, s);
     });
   });
@@ -1206,14 +1263,20 @@ int run_of(long long blocks, int most, int warps) {
   return run;
 }
 
-cudaError_t launch_adamw(const AwTable& t, const AwHyper& h, cudaStream_t s) { return launch_step<false>(t, h, s); }
-cudaError_t launch_adamw8(const AwTable& t, const AwHyper& h, cudaStream_t s) { return launch_step<true>(t, h, s); }
+cudaError_t launch_adamw(const AwTable& t, const AwHyper& h, cudaStream_t s) { return launch_step<false, false>(t, h, s); }
+cudaError_t launch_adamw8(const AwTable& t, const AwHyper& h, cudaStream_t s) {
+  return h.first ? launch_step<true, true>(t, h, s) : launch_step<true, false>(t, h, s);
+}
 
-cudaError_t launch_pack(const AwTable& t, const AwHyper& h, cudaStream_t s) {
+template <bool FIRST>
+cudaError_t launch_pack_of(const AwTable& t, const AwHyper& h, cudaStream_t s) {
   return with_wide_type(t.t[0].gt, [&](auto* m) {
-    const void* forms[2][2] = MO_FORMS(pack_kernel, Pointee<decltype(m)>);
+    const void* forms[2][2] = MO_FORMS(pack_kernel, FIRST, Pointee<decltype(m)>);
     return launch_list(forms, PK_MOMENTS, t, t.runs, h, s);
   });
+}
+cudaError_t launch_pack(const AwTable& t, const AwHyper& h, cudaStream_t s) {
+  return h.first ? launch_pack_of<true>(t, h, s) : launch_pack_of<false>(t, h, s);
 }
 
 cudaError_t launch_unpack(const AwTable& t, cudaStream_t s) {

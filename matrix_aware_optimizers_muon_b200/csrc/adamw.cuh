@@ -56,6 +56,7 @@ struct AwHyper {
   float lr, rate, root;            // lr, lr / (1 - b1^t), 1 / sqrt(1 - b2^t) of a step given by the host
   float log_b1, log_b2;            // for a step read on the device
   int bias, stochastic;
+  int first;                       // 8-bit moments: the first is rounded stochastically too
   unsigned long long seed;
   long long step;
   const float* lr_dev;

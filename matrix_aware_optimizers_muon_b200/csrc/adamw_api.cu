@@ -121,6 +121,9 @@ class Tables {
   int open_[2][4][4];              // the table that takes the next such tensor
 };
 
+// Whether the first of two 8-bit moments takes noise (see mo_adamw_cfg).
+bool first_by_noise(int stochastic) { return stochastic != 0 && stochastic != 2; }
+
 bool finite_nonneg(double x) { return std::isfinite(x) && x >= 0.0; }
 
 AwHyper hyper(const mo_adamw_cfg& c, int64_t step) {
@@ -146,6 +149,7 @@ AwHyper hyper(const mo_adamw_cfg& c, int64_t step) {
     h.root = (float)(1.0 / std::sqrt(-std::expm1((double)step * std::log(c.beta2))));
   }
   h.stochastic = c.stochastic != 0;
+  h.first = first_by_noise(c.stochastic);
   h.seed = c.seed;
   h.step = step;
   h.lr_dev = c.lr_dev;
@@ -380,6 +384,7 @@ cudaError_t run_pack(mo_ctx* ctx, const mo_list& l, const mo_pack_cfg& cfg, void
   if (!aligned(cfg.step_dev, 8)) refuse("device scalars must be aligned to their type");
   if (in_written(l, cfg.step_dev)) refuse("buffers overlap");
   h.stochastic = cfg.stochastic != 0;
+  h.first = first_by_noise(cfg.stochastic);
   h.seed = cfg.seed;
   h.step = cfg.step;
   h.step_dev = reinterpret_cast<const long long*>(cfg.step_dev);

@@ -16,8 +16,8 @@ elements, taken from the exponent E of the block's largest finite magnitude
     v: 5 exponent bits (bias 15), 3 mantissa bits, no sign, s = max(1, E - 15);
        255 stands for a value that is not finite; v > 0 has a code of at least 1
 
-m goes to the nearest code (ties to even), v to the nearest or, with noise bits
-u in 0..65535, to the code above where its distance from the code below, in
+m and v go to the nearest code (ties to even) or, with noise bits u in 0..65535,
+to the code above (in magnitude) where the distance from the code below, in
 steps, plus (16 u + 8) / 2^20 reaches one.  The moments that a step rounds are
 fp32 values, each product and sum of the recurrence rounded once
 (``fp32_moments``): with few-bit codes and 16-bit gradients the exact sum is
@@ -73,13 +73,24 @@ def _words(elements, seed, step, index):
     x ^= x >> np.uint64(16)
     y = ((x ^ k1) * b + k2) & low
     y ^= y >> np.uint64(16)
-    return x, y
+    z = ((x ^ k2) * a + k1) & low
+    z ^= z >> np.uint64(16)
+    return x, y, z
+
+
+def _halves(words, elements):
+    half = (np.asarray(elements, dtype=np.uint64) & np.uint64(1)) * np.uint64(16)
+    return tuple(((w >> half) & np.uint64(0xFFFF)).astype(np.int64) for w in words)
 
 
 def noise(elements, *, seed, step, index):
     """16 bits for each element's second moment and 16 for its bf16 weight."""
-    half = (np.asarray(elements, dtype=np.uint64) & np.uint64(1)) * np.uint64(16)
-    return tuple(((w >> half) & np.uint64(0xFFFF)).astype(np.int64) for w in _words(elements, seed, step, index))
+    return _halves(_words(elements, seed, step, index)[:2], elements)
+
+
+def first_noise(elements, *, seed, step, index):
+    """16 bits for each element's first moment."""
+    return _halves(_words(elements, seed, step, index)[2:], elements)[0]
 
 
 # ---------------------------------------------------------------- 8-bit codes
@@ -125,14 +136,15 @@ def _steps(x, bias):
     return x / np.ldexp(1.0, e - 3), (e + bias - 1) * 8
 
 
-def first_codes(m):
-    """(codes, scales) of the first moment."""
+def first_codes(m, bits=None):
+    """(codes, scales) of the first moment; bits: noise for stochastic rounding."""
     m = np.asarray(m, dtype=np.float64).reshape(-1)
     s = scale_bytes(m, 7)
     y = m / per_element(s, m.size)
     ok = np.isfinite(y)
     n, base = _steps(np.abs(np.where(ok, y, 0.0)), 7)
-    c = np.rint(n).astype(np.int64) + base + 128 * np.signbit(y)
+    n = np.rint(n) if bits is None else np.floor(n + (16 * bits + 8) / 2.0 ** 20)
+    c = n.astype(np.int64) + base + 128 * np.signbit(y)
     return np.where(ok, c, 127).astype(np.uint8), s
 
 
@@ -153,6 +165,21 @@ def first_moment(codes, scales):
 
 def second_moment(codes, scales):
     return second_values()[codes] * per_element(scales, codes.size)
+
+
+def adamw8_step(W, G, state, *, t, noise_seed=None, index=0, beta1=0.9, beta2=0.999, **hyper):
+    """(W, state) after one step with the moments held as codes, state = (M8, MS, V8, VS); with a noise_seed both are
+    rounded stochastically.  W is formed from the new moments before they are rounded to codes."""
+    m8, ms, v8, vs = state
+    M, V = first_moment(m8, ms), second_moment(v8, vs)
+    W = adamw_step(W, G, M, V, t=t, beta1=beta1, beta2=beta2, **hyper)[0]
+    m, v = fp32_moments(G, M, V, beta1, beta2)
+    mbits = vbits = None
+    if noise_seed is not None:
+        at = np.arange(m8.size)
+        mbits = first_noise(at, seed=noise_seed, step=t, index=index)
+        vbits = noise(at, seed=noise_seed, step=t, index=index)[0]
+    return W, (*first_codes(m, mbits), *second_codes(v, vbits))
 
 
 # ---------------------------------------------------------------- clipping
