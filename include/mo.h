@@ -478,6 +478,7 @@ MO_API mo_status adamw8_unpack(mo_ctx* ctx, const mo_adamw8_moments* list, int n
  * to max_norm at most ("LLM Optimizers", sections 7.4 and 7.5):
  *   norm   = || s G ||             (s = *scale, 1 when NULL)
  *   factor = s min(1, max_norm / (norm + 1e-6))
+ * formed in fp64 and rounded to fp32 once each.
  * With apply != 0 out_i = factor G_i, rounded to nearest in out's type; out == NULL
  * (or out == G) scales G_i in place.  With an out in fp32, 16-bit gradients
  * become the fp32 matrices that muon_step and soap_step take.  With apply == 0

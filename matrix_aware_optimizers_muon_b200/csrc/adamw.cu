@@ -1115,13 +1115,16 @@ __global__ void __launch_bounds__(AW_THREADS) norm_kernel(const __grid_constant_
   if (threadIdx.x == 0) partial[blockIdx.x] = s;
 }
 
-// The factor from the sum of all squares; the caller with `write` stores the results.
+// The factor from the sum of all squares, rounded to fp32 once; the caller with
+// `write` stores the results.
 __device__ __forceinline__ float factor_of(const ClipArgs& a, double squares, bool write) {
   const float scale = a.scale ? *a.scale : 1.f;
-  const float norm = (float)(fabs((double)scale) * sqrt(squares));
-  const float f = a.max_norm / (norm + 1e-6f);
+  const double exact = fabs((double)scale) * sqrt(squares);
+  const float norm = (float)exact;
+  // a norm that fp32 does not hold counts as infinite here too
+  const double f = (double)a.max_norm / ((isfinite(norm) ? exact : (double)norm) + 1e-6);
   // a norm that is not a number gives such a factor (1 only where f >= 1)
-  const float factor = scale * (f >= 1.f ? 1.f : f);
+  const float factor = (float)((double)scale * (f >= 1.0 ? 1.0 : f));
   if (write) {
     *a.norm = norm;
     *a.factor = factor;
