@@ -483,8 +483,9 @@ MO_API mo_status adamw8_unpack(mo_ctx* ctx, const mo_adamw8_moments* list, int n
  * (or out == G) scales G_i in place.  With an out in fp32, 16-bit gradients
  * become the fp32 matrices that muon_step and soap_step take.  With apply == 0
  * only norm and factor are written; adamw_step takes the factor as grad_scale.
- *  - Squares are taken in fp32, summed eight at a time in fp32 and from there
- *    on in fp64, in an order that the list and the number of SMs fix.
+ *  - Squares are taken in fp32 and summed eight at a time in fp32, from there on
+ *    in fp64; where they leave fp32's range or are so small that it loses bits of
+ *    them the squares are taken in fp64 too.  The order is one that the list and the number of SMs fix.
  *  - Nothing is special about a norm that is not finite (the factor is then 0
  *    or a NaN); *nonfinite tells it, for adamw_step's skip.
  *  - The partial sums are in the attached workspace (MO_CLIP_WORKSPACE_BYTES

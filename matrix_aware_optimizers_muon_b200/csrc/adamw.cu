@@ -1067,8 +1067,8 @@ __global__ void __launch_bounds__(AW_THREADS) unpack_kernel(const __grid_constan
 }
 
 // ---------------------------------------------------------------- clipping
-// norm    sum of squares: 8 at a time in fp32, then fp64; one partial sum per
-//         CTA, in an order that the grid alone fixes
+// norm    sum of squares: 8 at a time in fp32 (in fp64 where fp32 does not hold
+//         them), then fp64; one partial sum per CTA, in an order that the grid alone fixes
 // finish  the partial sums in a fixed order, the norm and the factor
 // scale   out = factor * G, the last runs first: L2 still holds them.  With few
 //         partial sums every CTA sums them itself and `finish` is left out.
@@ -1078,31 +1078,66 @@ __device__ __forceinline__ double warp_sum(double x) {
   return x;
 }
 
+// A lane's squares of a run, 64 at most, lose less than 2^-143 below fp32's
+// smallest numbers: under 2^-43 of a sum from here on.
+constexpr double LEAST_SQUARES = 0x1p-100;
+
+__device__ __forceinline__ float wide(float x) { return x; }
+__device__ __forceinline__ float wide(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float wide(__half x) { return __half2float(x); }
+
+// A lane's part of a run's sum of squares in fp64.
+template <typename T>
+__device__ __noinline__ double squares64(const T* g, int elements) {
+  double s = 0.0;
+  for (int i = threadIdx.x; i < elements; i += 32) {
+    const double x = wide(g[i]);
+    s += x * x;
+  }
+  return s;
+}
+
 template <typename T>
 struct NormOp {
   static constexpr bool AHEAD = false;
   static constexpr int BATCH = 4;                // with the scaling pass, 50 M elements: 67 us; with 1 76, with 8 69
   static constexpr bool BACKWARDS = false;
   using Load = Raw<T>;
-  double sum = 0.0;
+  double sum = 0.0, run;
   const T* g;
-  __device__ __forceinline__ void start(const AwTensor& t, unsigned long long first, int) { g = static_cast<const T*>(t.G) + first; }
+  long long left;                                // elements of the tensor from the run on
+  unsigned any;                                  // bits of the lane's elements: not all zeros, as unseen rows are
+  __device__ __forceinline__ void start(const AwTensor& t, unsigned long long first, int) {
+    g = static_cast<const T*>(t.G) + first;
+    left = t.numel - (long long)first;
+    run = 0.0;
+    any = 0;
+  }
   template <int AT, int WIDE = 1>
   __device__ __forceinline__ void fetch(Load& in, unsigned at, const Place<WIDE>& b = {}) const { mo::fetch<WIDE, AT>(in, g + at, b); }
   template <int WIDE>
   __device__ __forceinline__ void work(const Load& in, const Place<WIDE>&, unsigned at, int) {
     float x[PER], s = 0.f;
-    widen_all(x, settled<WIDE>(in, g + at));
+    const Load raw = settled<WIDE>(in, g + at);
+    widen_all(x, raw);
 #pragma unroll
     for (int j = 0; j < PER; ++j) s = fmaf(x[j], x[j], s);
-    sum += (double)s;
+#pragma unroll
+    for (int k = 0; k < Load::WORDS; ++k) any |= raw.w[k];
+    run += (double)s;
   }
   __device__ __forceinline__ void narrow(const AwTensor&, const Place<0>& b, unsigned at, int r) {
     Load in;
     fetch<0, 0>(in, at, b);
     work(in, b, at, r);
   }
-  __device__ __forceinline__ void finish(int) const {}
+  // A run whose squares fp32 does not hold is read again.
+  __device__ __forceinline__ void finish(int blocks) {
+    const unsigned some = any & (sizeof(T) == 2 ? 0x7fff7fffu : 0x7fffffffu);
+    const bool odd = !(run < (double)__uint_as_float(INF_BITS)) || (run < LEAST_SQUARES && some != 0);
+    if (rare(__any_sync(0xffffffffu, odd))) run = squares64(g, (int)min((long long)blocks * AW_BLOCK, left));
+    sum += run;
+  }
 };
 
 template <typename T, bool VEC, int N>

@@ -9,6 +9,7 @@ from oracle import adamw as oa
 
 pytestmark = pytest.mark.gpu
 
+
 def test_factor_is_rounded_once():
     """Norms that are whole numbers of 5 are exact; the factor is the fp32 value nearest to 1 / (norm + 1e-6)."""
     import torch
@@ -20,3 +21,46 @@ def test_factor_is_rounded_once():
         got.append(float(factor))
     want = np.float32(1.0 / (5.0 * np.arange(1, 101) + 1e-6))
     np.testing.assert_array_equal(np.float32(got), want)
+# ---------------------------------------------------------------- the norm over fp32's range
+
+
+def _norm_case(arrays, dtype, shift, scale=None):
+    """Squares are taken in fp32 and eight of them added (8 u of the sum: 4 u of the norm), or in fp64 where they would
+    leave fp32's range; the norm is rounded once more.  The factor is formed in fp64 and rounded once."""
+    import torch
+    ctx = context()
+    G = Flat(arrays, _dt(dtype), shift)
+    g0 = [_np(v) for v in G.views]
+    s = None if scale is None else torch.tensor(scale, device="cuda")
+    flag = torch.full((1,), 5, dtype=torch.int32, device="cuda")
+    norm, factor = ctx.clip_grads(list(G.views), 1.0, apply=False, scale=s, nonfinite=flag)
+    want, f = oa.clip(g0, 1.0, 1.0 if scale is None else float(np.float32(scale)))
+    if want > np.finfo(np.float32).max:               # of 1e37: finite gradients whose norm fp32 does not hold
+        assert int(flag) == 1 and np.isposinf(float(norm)) and float(factor) == 0
+        return
+    assert int(flag) == 0
+    assert abs(float(norm) - want) <= 6 * U * want + 2.0 ** -150, (float(norm), want)
+    assert abs(float(factor) - f) <= 6 * U * f, (float(factor), f)
+
+
+@pytest.mark.parametrize("shift", [0, 1])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("size", [8e18, 1e19, 1e30, 1e37, 1e-19, 1e-22, 1e-30, 1e-38])
+def test_norm_of_large_and_small_gradients(dtype, shift, size):
+    rng = np.random.default_rng(1)
+    _norm_case([size * rng.uniform(0.5, 1, n) for n in (8, 5000, 256, 3)], dtype, shift)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_norm_of_blocks_of_every_size(dtype):
+    rng = np.random.default_rng(2)
+    x = rng.standard_normal(256 * 40) * np.repeat(10.0 ** rng.uniform(-44, 19, 256 * 5), 8)
+    _norm_case([x, x[:700] * 1e17], dtype, 0)
+    _norm_case([x[:3001] * 1e-18, np.full(9, 1e-42), np.zeros(300)], dtype, 1)
+
+
+def test_norm_with_a_scale_that_brings_it_back():
+    """The scale is applied to the norm in fp64: gradients that were scaled up for fp16 may be large."""
+    rng = np.random.default_rng(3)
+    _norm_case([1e25 * rng.standard_normal(4000)], "f32", 0, 2.0 ** -80)
+    _norm_case([1e-30 * rng.standard_normal(4000)], "f32", 0, 2.0 ** 90)
