@@ -275,11 +275,18 @@ bool touches(const mo_list& l, const void* p, size_t bytes) {
   return false;
 }
 
-// Whether p is in memory that the list writes (which no other range of it meets).
-bool in_written(const mo_list& l, const void* p) {
-  const uintptr_t at = reinterpret_cast<uintptr_t>(p);
-  auto x = std::upper_bound(l.ranges.begin(), l.ranges.end(), at, [](uintptr_t a, const Range& b) { return a < b.lo; });
-  return x != l.ranges.begin() && (--x)->written && at < x->hi;
+// Whether [p, p + bytes) meets memory that the list writes.  No other range of
+// the list meets that: behind the first range that begins before p there is none.
+bool in_written(const mo_list& l, const void* p, size_t bytes) {
+  if (p == nullptr) return false;
+  const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+  auto x = std::lower_bound(l.ranges.begin(), l.ranges.end(), lo + bytes, [](const Range& a, uintptr_t b) { return a.lo < b; });
+  while (x != l.ranges.begin()) {
+    --x;
+    if (x->written && lo < x->hi) return true;
+    if (x->lo < lo) return false;
+  }
+  return false;
 }
 
 template <typename T, typename F>
@@ -369,9 +376,9 @@ const T& given(const T* cfg) {
 
 cudaError_t run_adamw(mo_ctx* ctx, const mo_list& l, const mo_adamw_cfg& cfg, int64_t step, void* stream) {
   const AwHyper h = hyper(cfg, step);
-  const void* scalars[] = {cfg.lr_dev, cfg.step_dev, cfg.grad_scale, cfg.skip};
-  for (const void* p : scalars)
-    if (in_written(l, p)) refuse("buffers overlap");
+  if (in_written(l, cfg.lr_dev, 4) || in_written(l, cfg.step_dev, 8) || in_written(l, cfg.grad_scale, 4) ||
+      in_written(l, cfg.skip, 4))
+    refuse("buffers overlap");
   const bool eight = l.kind == LIST_ADAMW8;
   return launch_all(ctx, l.tabs, [&](const AwTable& tab) {
     return eight ? launch_adamw8(tab, h, static_cast<cudaStream_t>(stream))
@@ -382,7 +389,7 @@ cudaError_t run_adamw(mo_ctx* ctx, const mo_list& l, const mo_adamw_cfg& cfg, in
 cudaError_t run_pack(mo_ctx* ctx, const mo_list& l, const mo_pack_cfg& cfg, void* stream) {
   AwHyper h = {};
   if (!aligned(cfg.step_dev, 8)) refuse("device scalars must be aligned to their type");
-  if (in_written(l, cfg.step_dev)) refuse("buffers overlap");
+  if (in_written(l, cfg.step_dev, 8)) refuse("buffers overlap");
   h.stochastic = cfg.stochastic != 0;
   h.first = first_by_noise(cfg.stochastic);
   h.seed = cfg.seed;
