@@ -735,8 +735,9 @@ __device__ __forceinline__ Rates rates_of(const AwHyper& h, const AwTensor& t) {
 // sqrt and reciprocal of the special-function unit (2^-23 relative each): the
 // update they scale is a small part of the weight.  The
 // forms that take subnormal numbers as zeros need two instructions, the others
-// ten; they change a denominator by less than 2^-63 / sqrt(1 - b2), which is
-// nothing beside any eps of 1e-10 or more.
+// ten; they change a denominator by less than 2^-63 root, which is below 2^-26 of
+// an eps of 2^-37 root or more, and have no reciprocal for denominators above
+// 2^126, which sqrt(v) root (2^64 2^27 at most) does not reach.
 template <bool TINY>
 __device__ __forceinline__ float sqrt_fast(float x) {
   float r;
@@ -772,7 +773,7 @@ __device__ __forceinline__ void update(float (&w)[PER], float (&m)[PER], float (
     m[j] = __fadd_rn(__fmul_rn(b1, m[j]), __fmul_rn(h.c1, g[j]));
     v[j] = __fadd_rn(__fmul_rn(b2, v[j]), __fmul_rn(h.c2, __fmul_rn(g[j], g[j])));
   }
-  if (rare(h.eps < 1e-10f)) new_weights<true>(w, m, v, r, h.eps);
+  if (rare(!(h.eps >= 0x1p-37f * r.root && h.eps <= 0x1p100f))) new_weights<true>(w, m, v, r, h.eps);
   else new_weights<false>(w, m, v, r, h.eps);
 }
 

@@ -64,3 +64,30 @@ def test_norm_with_a_scale_that_brings_it_back():
     rng = np.random.default_rng(3)
     _norm_case([1e25 * rng.standard_normal(4000)], "f32", 0, 2.0 ** -80)
     _norm_case([1e-30 * rng.standard_normal(4000)], "f32", 0, 2.0 ** 90)
+
+
+# ---------------------------------------------------------------- denominators at the ends of fp32
+
+
+@pytest.mark.parametrize("device", [False, True])
+@pytest.mark.parametrize("b2,eps,size", [(1 - 1e-7, 1e-10, 2e-16), (1 - 1e-10, 1e-9, 6e-15), (0.999, 1e-10, 2e-18), (0.999, 1.5e38, 1e18),
+                                         (0.999, 2.0 ** 101, 1e18)])
+def test_small_second_moments_and_large_eps(b2, eps, size, device):
+    """The first step from zero moments: V = (1 - b2) g^2 around fp32's smallest normal number, divided by 1 - b2 again, beside
+    eps; and a denominator whose reciprocal is below it.  The bounds of the steps of test_gpu_adamw.py."""
+    import torch
+    ctx = context()
+    n = 2000
+    rng = np.random.default_rng(4)
+    g = np.float64(np.float32(size * np.exp(rng.uniform(-1, 1, n)) * rng.choice([-1, 1], n)))
+    W, M, V = (torch.zeros(n, device="cuda") for _ in range(3))
+    step, lr = 1, 1.0
+    if device:
+        step, lr = torch.tensor([1], device="cuda"), torch.tensor(1.0, device="cuda")
+    ctx.adamw_step([dict(W=W, G=torch.from_numpy(g).float().cuda(), M=M, V=V)], step, lr=lr, beta2=b2, eps=eps)
+    # V as fp32 holds it: below 2^-126 its own rounding is larger than u
+    v = np.float64(np.float32(1 - b2) * np.float32(np.float32(g) * np.float32(g)))
+    m = np.float64(np.float32(0.1) * np.float32(g))
+    D = (m / 0.1) / (np.sqrt(v / (1 - b2)) + eps)
+    got = _np(W)
+    assert np.all(np.abs(got + D) <= U * 24 * np.abs(D) + 1e-45), np.max(np.abs(got + D) / np.abs(D)) / U
