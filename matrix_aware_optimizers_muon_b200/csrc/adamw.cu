@@ -601,21 +601,25 @@ __device__ __forceinline__ unsigned pack_tops(unsigned a, unsigned b, unsigned c
   return __byte_perm(__byte_perm(a, b, 0x0073), __byte_perm(c, d, 0x0073), 0x5410);
 }
 
-// Codes of v in bits 24 to 31 of r; scaled is v times 2^(127 - s) 2^-112.
+// Codes of v in bits 24 to 31 of r; vi is 2^(127 - s) 2^-112 of what v is in.  A
+// subnormal product is cut off, which the noise does not see (see first_codes).  To
+// nearest it must not be rounded before the code is: codes up to 8, which are the
+// whole numbers of steps of 2^(s - 127) 2^-17, are formed again by a conversion.
 template <bool STOCHASTIC, int WIDE>
-__device__ __forceinline__ void second_codes(unsigned (&r)[PER], const float (&v)[PER], const float (&scaled)[PER],
-                                             const Noise<WIDE>& n) {
+__device__ __forceinline__ void second_codes(unsigned (&r)[PER], const float (&v)[PER], float vi, const Noise<WIDE>& n) {
   unsigned least = 0xffffffffu;
 #pragma unroll
   for (int j = 0; j < PER; ++j) {
-    const unsigned u = __float_as_uint(scaled[j]);
+    const unsigned u = __float_as_uint(__fmul_rz(v[j], vi));
     r[j] = STOCHASTIC ? u * 16u + n.bits24(j) : (u + 0x7ffffu + ((u >> 20) & 1u)) * 16u;
     least = min(least, r[j]);
   }
-  if (rare(least < (1u << 24))) {
+  if (rare(least < (STOCHASTIC ? 1u << 24 : 9u << 24))) {
 #pragma unroll
-    for (int j = 0; j < PER; ++j)
+    for (int j = 0; j < PER; ++j) {
+      if (!STOCHASTIC && r[j] < (9u << 24)) r[j] = __float2uint_rn(v[j] * (vi * 0x1p112f) * 0x1p17f) << 24;
       if (v[j] > 0.f && r[j] < (1u << 24)) r[j] = 1u << 24;
+    }
   }
 }
 
@@ -652,17 +656,13 @@ __device__ __forceinline__ void store_moments(float (&m)[PER], float (&v)[PER], 
   unsigned um = __reduce_max_sync(0xffffffffu, __float_as_uint(bm));
   unsigned uv = __reduce_max_sync(0xffffffffu, bv);
   unsigned odd = 0;                                    // elements whose v has code 255
-  float scaled[PER];
   unsigned ms, vs;
-  float mi;                                            // FIRST: 2^(127 - s) 2^-120, a normal number below FIRST_HIGH_BITS
+  float mi, vi;       // 2^(127 - s) 2^-120 (FIRST) and 2^(127 - s) 2^-112, normal numbers below FIRST_HIGH_BITS and HIGH_BITS
   if (!rare(um >= (FIRST ? FIRST_HIGH_BITS : INF_BITS) || uv >= HIGH_BITS)) {
     ms = max(1, (int)(um >> 23) - 7);
     mi = __uint_as_float(((FIRST ? 134u : 254u) - ms) << 23);
     vs = max(1, (int)(uv >> 23) - 15);
-    const float vi = __uint_as_float((142u - vs) << 23);   // 2^(127 - s) 2^-112, a normal number below HIGH_BITS
-#pragma unroll
-    for (int j = 0; j < PER; ++j) scaled[j] = v[j];
-    scale_all(scaled, vi);
+    vi = __uint_as_float((142u - vs) << 23);
   } else {
     // the scale is that of the finite values; an infinite m has no code and becomes a NaN
     um = uv = 0;
@@ -677,8 +677,11 @@ __device__ __forceinline__ void store_moments(float (&m)[PER], float (&v)[PER], 
     uv = __reduce_max_sync(0xffffffffu, uv);
     ms = max(1, (int)(um >> 23) - 7);
     vs = max(1, (int)(uv >> 23) - 15);
+    // scaled in two steps: what the first cuts off below 2^-126 is far below any code, but it stays above 0
 #pragma unroll
-    for (int j = 0; j < PER; ++j) scaled[j] = v[j] * __uint_as_float((254u - vs) << 23) * 0x1p-112f;
+    for (int j = 0; j < PER; ++j)
+      if (v[j] > 0.f) v[j] = fmaxf(v[j] * __uint_as_float((254u - vs) << 23), 0x1p-149f);
+    vi = 0x1p-112f;
     mi = __uint_as_float((254u - ms) << 23);
     if constexpr (FIRST) {
       scale_all(m, mi);
@@ -699,8 +702,8 @@ __device__ __forceinline__ void store_moments(float (&m)[PER], float (&v)[PER], 
 #pragma unroll
     for (int q = 0; q < PER / 4; ++q) mw[q] = __byte_perm(pair(4 * q), pair(4 * q + 2), 0x5410);
   }
-  if (FIRST || stochastic) second_codes<true>(vr, v, scaled, n);
-  else second_codes<false>(vr, v, scaled, n);
+  if (FIRST || stochastic) second_codes<true>(vr, v, vi, n);
+  else second_codes<false>(vr, v, vi, n);
   if (rare(odd != 0)) {
 #pragma unroll
     for (int j = 0; j < PER; ++j)

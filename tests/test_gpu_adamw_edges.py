@@ -91,3 +91,52 @@ def test_small_second_moments_and_large_eps(b2, eps, size, device):
     D = (m / 0.1) / (np.sqrt(v / (1 - b2)) + eps)
     got = _np(W)
     assert np.all(np.abs(got + D) <= U * 24 * np.abs(D) + 1e-45), np.max(np.abs(got + D) / np.abs(D)) / U
+
+
+# ---------------------------------------------------------------- codes below the normal ones
+
+
+def _low_codes(values, top):
+    """A block whose scale is 1 (its largest value is `top`) and which holds `values`."""
+    x = np.zeros(256, dtype=np.float32)
+    x[0] = top
+    x[1:1 + len(values)] = values
+    assert np.all(np.float64(x[1:1 + len(values)]) == values)
+    return x
+
+
+def test_second_codes_next_to_ties():
+    """V at one fp32 step from the middle between two codes: the nearest code is that of the value, not of the value
+    rounded to the bits that an fp32 number of its size would have below 2^-126."""
+    import torch
+    ctx = context()
+    near = [(c + 0.5) * (1 + s * 2.0 ** -23) * 2.0 ** -17 for c in range(1, 8) for s in (-1, 0, 1)]
+    near = [float(np.float32(x)) for x in near] + [float(np.nextafter(np.float32((c + 0.5) * 2.0 ** -17), np.float32(s)))
+                                                   for c in range(1, 8) for s in (0, 1)]
+    for top in (2.0 ** 15, 2.0 ** 15 * 2.0 ** 100, 2.0 ** 15 * 2.0 ** -60):
+        x = _low_codes(np.array(near) * (top / 2.0 ** 15), top)
+        M, V = torch.zeros(256, device="cuda"), torch.from_numpy(x).cuda()
+        d = ctx.adamw8_state(M)
+        ctx.adamw8_pack([dict(M=M, V=V, **d)])
+        np.testing.assert_array_equal(d["V8"].cpu().numpy(), oa.second_codes(x)[0])
+
+
+def test_noise_next_to_a_code():
+    """Values that the noise brings to less than one fp32 step below a code, and just to it."""
+    import torch
+    ctx = context()
+    for kw, kind in ((dict(seed=3), "second"), (dict(noise=3), "second"), (dict(noise=3), "first")):
+        at = np.arange(256)
+        first = kind == "first"
+        bits = oa.first_noise(at, seed=3, step=5, index=0) if first else oa.noise(at, seed=3, step=5, index=0)[0]
+        # c + 1 - (16 bits + 8) / 2^20 is a code's border; a quarter of 2^-20 below it, at it, and above it
+        border = (at % 6 + 2) - (16.0 * bits + 8) / 2 ** 20
+        y = border + np.array([-0.5, 0.0, 0.5])[at % 3] / 2 ** 20
+        unit, top = (2.0 ** -9, 2.0 ** 7) if first else (2.0 ** -17, 2.0 ** 15)
+        x = np.float32(y * unit)
+        x[0] = top
+        X, Z = torch.from_numpy(x).cuda(), torch.zeros(256, device="cuda")
+        d = ctx.adamw8_state(Z)
+        ctx.adamw8_pack([dict(M=X if first else Z, V=Z if first else X, **d)], step=5, **kw)
+        want = oa.first_codes(x, bits)[0] if first else oa.second_codes(x, bits)[0]
+        np.testing.assert_array_equal(d["M8" if first else "V8"].cpu().numpy(), want)
