@@ -820,17 +820,17 @@ struct Shared {
 };
 
 __device__ __forceinline__ void moments_of(float (&m)[PER], float (&v)[PER], const Raw<float>& mr, const Raw<float>& vr, float&,
-                                           float&, unsigned) {
+                                           float&, unsigned, unsigned) {
   widen_all(m, mr);
   widen_all(v, vr);
 }
 __device__ __forceinline__ void moments_of(float (&m)[PER], float (&v)[PER], const Raw<Code>& mc, const Raw<Code>& vc, float& ms,
-                                           float& vs, unsigned scales) {
+                                           float& vs, unsigned scales, unsigned least) {
   decode(m, v, mc, vc);
   const unsigned msb = scales & 0xffu, vsb = scales >> 8;
   ms = scale_of(msb);
   vs = scale_of(vsb);
-  if (rare(min(msb, vsb) < 32)) {
+  if (rare(min(msb, vsb) < least)) {
     // b1 ms or b2 vs may be subnormal and not exact: scale the moments themselves
     scale_all(m, ms);
     scale_all(v, vs);
@@ -895,7 +895,7 @@ struct StepOp {
     widen_all(w1, settled<WIDE>(in.w, w + at));
     if (h.gscale != nullptr) scale_all(g1, gs);
     float sm = 1.f, sv = 1.f;
-    moments_of(m1, v1, settled<WIDE>(in.m, m + at), settled<WIDE>(in.v, v + at), sm, sv, EIGHT ? scales.of(r) : 0);
+    moments_of(m1, v1, settled<WIDE>(in.m, m + at), settled<WIDE>(in.v, v + at), sm, sv, EIGHT ? scales.of(r) : 0, h.least_scale);
     update(w1, m1, v1, g1, h, s.r, sm, sv);
     constexpr bool LOW = sizeof(WT) == 2;
     Noise<WIDE> n;

@@ -57,6 +57,7 @@ struct AwHyper {
   float log_b1, log_b2;            // for a step read on the device
   int bias, stochastic;
   int first;                       // 8-bit moments: the first is rounded stochastically too
+  unsigned least_scale;            // scale byte from which on betas times the scale are normal numbers
   unsigned long long seed;
   long long step;
   const float* lr_dev;

@@ -137,6 +137,9 @@ AwHyper hyper(const mo_adamw_cfg& c, int64_t step) {
   h.c1 = (float)(1.0 - c.beta1);
   h.b2 = (float)c.beta2;
   h.c2 = (float)(1.0 - c.beta2);
+  h.least_scale = 32;                                  // 2^-95 times 2^-31 or more
+  for (float b : {h.b1, h.b2})
+    if (b > 0.f && b < 0x1p-31f) h.least_scale = 256;
   h.eps = (float)c.eps;
   h.lr = (float)c.lr;
   h.log_b1 = (float)std::log(c.beta1);

@@ -140,3 +140,25 @@ def test_noise_next_to_a_code():
         ctx.adamw8_pack([dict(M=X if first else Z, V=Z if first else X, **d)], step=5, **kw)
         want = oa.first_codes(x, bits)[0] if first else oa.second_codes(x, bits)[0]
         np.testing.assert_array_equal(d["M8" if first else "V8"].cpu().numpy(), want)
+
+
+def test_small_betas_keep_the_order_of_roundings():
+    """rn(b M) with a beta that times the scale of M is below fp32's normal numbers: 8 eighths times b stand 2^-20 above the
+    middle between two codes."""
+    import torch
+    ctx = context()
+    b = 2.0 ** -41 * (17 / 16 + 2.0 ** -23)
+    n = 512
+    W, G = torch.zeros(n, device="cuda"), torch.zeros(n, device="cuda")
+    st = ctx.adamw8_state(W)
+    st["M8"].copy_(torch.arange(n) % 8 + 8 * (torch.arange(n) // 8 % 15))
+    st["V8"].copy_(torch.arange(n) % 248)
+    st["MS"].fill_(40)
+    st["VS"].fill_(41)
+    c = {k: v.cpu().numpy() for k, v in st.items()}
+    m0, v0 = oa.first_moment(c["M8"], c["MS"]), oa.second_moment(c["V8"], c["VS"])
+    ctx.adamw8_step([dict(W=W, G=G, **st)], 1, beta1=b, beta2=b, noise=None)
+    m, v = oa.fp32_moments(0 * m0, m0, v0, b, b)
+    for key, (codes, scales) in (("M", oa.first_codes(m)), ("V", oa.second_codes(v))):
+        np.testing.assert_array_equal(st[key + "S"].cpu().numpy(), scales)
+        np.testing.assert_array_equal(st[key + "8"].cpu().numpy(), codes)
