@@ -200,7 +200,8 @@ class Context:
         return mn.value, full.value
 
     def attach_workspace(self, nbytes, stream=None):
-        """Allocate ``nbytes`` of device memory with torch and attach it.
+        """Allocate ``nbytes`` of device memory with torch, as memory of
+        ``stream``, and attach it.
 
         Library work already enqueued may still use a workspace this one
         replaces, on any stream, and the switch itself copies the old status
@@ -211,7 +212,8 @@ class Context:
         whenever the graph replays.  So a buffer replaced during capture is
         kept alive (``retired``) until the next attach outside capture."""
         import torch
-        buf = torch.empty(int(nbytes), dtype=torch.uint8, device=f"cuda:{self.device}")
+        with torch.cuda.stream(stream):         # else the current stream might still be writing it
+            buf = torch.empty(int(nbytes), dtype=torch.uint8, device=f"cuda:{self.device}")
         self._check(self.lib.mo_set_workspace(self.handle, c_void_p(buf.data_ptr()), buf.numel(),
                                               self._stream(stream)))
         old, self._workspace = self._workspace, buf

@@ -162,3 +162,26 @@ def test_small_betas_keep_the_order_of_roundings():
     for key, (codes, scales) in (("M", oa.first_codes(m)), ("V", oa.second_codes(v))):
         np.testing.assert_array_equal(st[key + "S"].cpu().numpy(), scales)
         np.testing.assert_array_equal(st[key + "8"].cpu().numpy(), codes)
+
+
+# ---------------------------------------------------------------- streams
+
+
+def test_workspace_of_a_first_call_on_another_stream():
+    """The workspace that a call on a given stream attaches is not memory that the current stream still writes."""
+    import torch
+    n = 1 << 20
+    want = float(np.sqrt(n))
+    G = torch.ones(n, device="cuda")
+    s = torch.cuda.Stream()
+    for _ in range(3):
+        ctx = context()
+        torch.cuda.synchronize()
+        old = [torch.empty(k, dtype=torch.uint8, device="cuda") for k in (4096, 65536, 256 + 65536, 1 << 20)]
+        torch.cuda._sleep(100_000_000)                 # some 50 ms
+        for x in old:
+            x.fill_(255)
+        del old, x
+        norm, _ = ctx.clip_grads([G], 1.0, apply=False, stream=s)
+        torch.cuda.synchronize()
+        assert float(norm) == want and ctx.device_status() == 0
