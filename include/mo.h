@@ -352,7 +352,8 @@ MO_API mo_status mo_soap_muon_workspace_bytes(mo_ctx* ctx, const mo_soap_muon_ma
  *   V <- b2 V + (1 - b2) g * g
  *   W <- (1 - lr' wd) W - lr' (M / (1 - b1^t)) / (sqrt(V / (1 - b2^t)) + eps)
  * with lr' = lr * lr_scale and wd = weight_decay of the tensor.  The whole list
- * takes one launch for each 350 tensors of one pair of types and no workspace.
+ * takes no workspace and one launch for each 350 tensors of one pair of types
+ * that are aligned for the wide path, and for each 350 that are not.
  *  - A tensor is numel contiguous elements at a pointer aligned to its
  *    element; numel 0 or G == NULL skips it.  The wide path needs pointers
  *    aligned to 8 elements (8-bit codes to 8 bytes) and gives the same bits.
@@ -485,7 +486,8 @@ MO_API mo_status adamw8_unpack(mo_ctx* ctx, const mo_adamw8_moments* list, int n
  * only norm and factor are written; adamw_step takes the factor as grad_scale.
  *  - Squares are taken in fp32 and summed eight at a time in fp32, from there on
  *    in fp64; where they leave fp32's range or are so small that it loses bits of
- *    them the squares are taken in fp64 too.  The order is one that the list and the number of SMs fix.
+ *    them the squares are taken in fp64 too.  The order is fixed by the list, by
+ *    its tensors' alignment and by the number of SMs of the context's GPU.
  *  - Nothing is special about a norm that is not finite (the factor is then 0
  *    or a NaN); *nonfinite tells it, for adamw_step's skip.
  *  - The partial sums are in the attached workspace (MO_CLIP_WORKSPACE_BYTES
@@ -521,7 +523,8 @@ MO_API mo_status clip_grads(mo_ctx* ctx, const mo_grad* list /* host array */, i
  * sizes, in host memory, and no contents.  A moments list serves adamw8_pack
  * and adamw8_unpack (none of its buffers may overlap another, in the calls with
  * arrays either).  Results and refusals are those of the calls with arrays;
- * *out is NULL after a refusal.  mo_list_destroy takes NULL. */
+ * *out is NULL after a refusal.  A list serves every context of the device it was
+ * made for; another device's refuses it.  mo_list_destroy takes NULL. */
 typedef struct mo_list mo_list;
 
 MO_API mo_status mo_adamw_list(mo_ctx* ctx, const mo_adamw_tensor* list, int n, mo_list** out);

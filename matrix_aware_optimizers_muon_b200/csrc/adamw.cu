@@ -1299,9 +1299,9 @@ cudaError_t launch_step(const AwTable& t, const AwHyper& h, cudaStream_t s) {
 //   300 odd ones, 8 bits (19 k blocks)     2: 40    4: 38       8: 48
 //   218 M elements, 8 bits, unpacking      1: 1759  4: 685      8: 622
 //   218 M elements, fp32                   1: 906   2: 903      8: 951
-int run_of(long long blocks, int most, int warps) {
+int run_of(long long blocks, int most, int warps, int sms) {
   int run = 1;
-  while (run < most && blocks >= (long long)warps * run * device_sm_count()) run *= 2;
+  while (run < most && blocks >= (long long)warps * run * sms) run *= 2;
   return run;
 }
 

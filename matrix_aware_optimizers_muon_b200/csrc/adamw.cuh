@@ -81,13 +81,13 @@ constexpr int CLIP_MAX_CTAS = 8192;   // partial sums of one call
 constexpr int FEW_PARTS = 512;        // partial sums that one warp takes
 constexpr int FINISH_THREADS = 256;
 
-// Blocks of a run, at most `most`, for a list of so many blocks: twice as long
-// while that leaves half of `warps` runs for each SM.
+// Blocks of a run, at most `most`, for a list of so many blocks on `sms` SMs: twice
+// as long while that leaves half of `warps` runs for each SM.
 // Steps and moments: 64 (see run_of).  Gradients, whose kernels take four blocks at
 // a time and where few runs mean few partial sums: 2 (65 tensors of 4096: 5.0 us
 // captured and 13.0 with the host; with 64 6.2 and 15.0).
 constexpr int STEP_RUNS = 64, GRAD_RUNS = 2;
-int run_of(long long blocks, int most, int warps);
+int run_of(long long blocks, int most, int warps, int sms);
 cudaError_t launch_adamw(const AwTable& t, const AwHyper& h, cudaStream_t s);
 cudaError_t launch_adamw8(const AwTable& t, const AwHyper& h, cudaStream_t s);
 cudaError_t launch_pack(const AwTable& t, const AwHyper& h, cudaStream_t s);

@@ -97,11 +97,11 @@ class Tables {
     tabs_[open]->t[tabs_[open]->n++] = t;
     blocks_[open] += blocks;
   }
-  // Divides the tensors into runs, once all are in.
-  void finish() {
+  // Divides the tensors into runs for a GPU of so many SMs, once all are in.
+  void finish(int sms) {
     for (size_t k = 0; k < tabs_.size(); ++k) {
       AwTable& tab = *tabs_[k];
-      tab.run = run_of(blocks_[k], most_run_, warps_);
+      tab.run = run_of(blocks_[k], most_run_, warps_, sms);
       tab.runs = 0;
       for (int i = 0; i < tab.n; ++i) {
         tab.t[i].first = tab.runs;
@@ -262,6 +262,7 @@ enum ListKind { LIST_ADAMW, LIST_ADAMW8, LIST_MOMENTS, LIST_GRADS };
 // A checked list with its launch tables.
 struct mo_list {
   mo::ListKind kind;
+  int device;
   mo::Tables tabs;
   std::vector<mo::Range> ranges;       // sorted
 };
@@ -293,20 +294,20 @@ bool in_written(const mo_list& l, const void* p, size_t bytes) {
 }
 
 template <typename T, typename F>
-std::unique_ptr<mo_list> build(ListKind kind, const T* list, int n, Tables tabs, F fill) {
+std::unique_ptr<mo_list> build(const mo_ctx* ctx, ListKind kind, const T* list, int n, Tables tabs, F fill) {
   if (n < 0) refuse("n < 0");
   if (n > 0 && list == nullptr) refuse("null list");
-  std::unique_ptr<mo_list> l(new mo_list{kind, std::move(tabs), {}});
+  std::unique_ptr<mo_list> l(new mo_list{kind, ctx_device(ctx), std::move(tabs), {}});
   l->ranges.reserve((size_t)n * 7);
   for (int i = 0; i < n; ++i)
     if (numel_ok(list[i].numel, i)) fill(list[i], i, *l);
   check_apart(l->ranges);
-  l->tabs.finish();
+  l->tabs.finish(device_sm_count(l->device));
   return l;
 }
 
-std::unique_ptr<mo_list> build_adamw(const mo_adamw_tensor* list, int n) {
-  return build(LIST_ADAMW, list, n, Tables(AW_RUN32), [](const mo_adamw_tensor& a, int i, mo_list& l) {
+std::unique_ptr<mo_list> build_adamw(const mo_ctx* ctx, const mo_adamw_tensor* list, int n) {
+  return build(ctx, LIST_ADAMW, list, n, Tables(AW_RUN32), [](const mo_adamw_tensor& a, int i, mo_list& l) {
     if (a.G == nullptr) return;
     AwTensor t = step_tensor(a, i, l.ranges);
     buffer(l.ranges, a.M, a.numel, 4, true, "M", i);
@@ -318,8 +319,8 @@ std::unique_ptr<mo_list> build_adamw(const mo_adamw_tensor* list, int n) {
   });
 }
 
-std::unique_ptr<mo_list> build_adamw8(const mo_adamw8_tensor* list, int n) {
-  return build(LIST_ADAMW8, list, n, Tables(AW_RUN), [](const mo_adamw8_tensor& a, int i, mo_list& l) {
+std::unique_ptr<mo_list> build_adamw8(const mo_ctx* ctx, const mo_adamw8_tensor* list, int n) {
+  return build(ctx, LIST_ADAMW8, list, n, Tables(AW_RUN), [](const mo_adamw8_tensor& a, int i, mo_list& l) {
     if (a.G == nullptr) return;
     AwTensor t = step_tensor(a, i, l.ranges);
     codes(a, i, l.ranges, t);
@@ -329,8 +330,8 @@ std::unique_ptr<mo_list> build_adamw8(const mo_adamw8_tensor* list, int n) {
 
 // One table serves both directions: pack reads M and V through G and C, unpack
 // writes them through W and C.
-std::unique_ptr<mo_list> build_moments(const mo_adamw8_moments* list, int n) {
-  return build(LIST_MOMENTS, list, n, Tables(AW_RUN), [](const mo_adamw8_moments& a, int i, mo_list& l) {
+std::unique_ptr<mo_list> build_moments(const mo_ctx* ctx, const mo_adamw8_moments* list, int n) {
+  return build(ctx, LIST_MOMENTS, list, n, Tables(AW_RUN), [](const mo_adamw8_moments& a, int i, mo_list& l) {
     if (a.type != MO_F32 && a.type != MO_BF16) refuse("type must be MO_F32 or MO_BF16" + at(i));
     AwTensor t = {};
     t.wt = t.gt = (AwType)a.type;
@@ -345,8 +346,8 @@ std::unique_ptr<mo_list> build_moments(const mo_adamw8_moments* list, int n) {
   });
 }
 
-std::unique_ptr<mo_list> build_grads(const mo_grad* list, int n) {
-  return build(LIST_GRADS, list, n, Tables(AW_RUN, GRAD_RUNS, true), [](const mo_grad& a, int i, mo_list& l) {
+std::unique_ptr<mo_list> build_grads(const mo_ctx* ctx, const mo_grad* list, int n) {
+  return build(ctx, LIST_GRADS, list, n, Tables(AW_RUN, GRAD_RUNS, true), [](const mo_grad& a, int i, mo_list& l) {
     if (a.G == nullptr) return;
     const bool in_place = a.out == nullptr || a.out == a.G;
     if (!type_ok(a.g_type) || (a.out != nullptr && !type_ok(a.out_type))) refuse("bad g_type or out_type" + at(i));
@@ -365,9 +366,10 @@ std::unique_ptr<mo_list> build_grads(const mo_grad* list, int n) {
   });
 }
 
-const mo_list& of_kind(const mo_list* l, ListKind kind) {
+const mo_list& of_kind(const mo_ctx* ctx, const mo_list* l, ListKind kind) {
   if (l == nullptr) refuse("null list");
   if (l->kind != kind) refuse("a list made for another call");
+  if (l->device != ctx_device(ctx)) refuse("a list made for another device");
   return *l;
 }
 
@@ -478,69 +480,69 @@ using namespace mo;
 extern "C" {
 
 mo_status mo_adamw_list(mo_ctx* ctx, const mo_adamw_tensor* list, int n, mo_list** out) {
-  return make_list(ctx, "adamw_step", out, [&]() { return build_adamw(list, n); });
+  return make_list(ctx, "adamw_step", out, [&]() { return build_adamw(ctx, list, n); });
 }
 mo_status mo_adamw8_list(mo_ctx* ctx, const mo_adamw8_tensor* list, int n, mo_list** out) {
-  return make_list(ctx, "adamw8_step", out, [&]() { return build_adamw8(list, n); });
+  return make_list(ctx, "adamw8_step", out, [&]() { return build_adamw8(ctx, list, n); });
 }
 mo_status mo_moments_list(mo_ctx* ctx, const mo_adamw8_moments* list, int n, mo_list** out) {
-  return make_list(ctx, "adamw8_moments", out, [&]() { return build_moments(list, n); });
+  return make_list(ctx, "adamw8_moments", out, [&]() { return build_moments(ctx, list, n); });
 }
 mo_status mo_grad_list(mo_ctx* ctx, const mo_grad* list, int n, mo_list** out) {
-  return make_list(ctx, "clip_grads", out, [&]() { return build_grads(list, n); });
+  return make_list(ctx, "clip_grads", out, [&]() { return build_grads(ctx, list, n); });
 }
 void mo_list_destroy(mo_list* list) { delete list; }
 
 mo_status adamw_step_list(mo_ctx* ctx, const mo_list* list, const mo_adamw_cfg* cfg, int64_t step, void* stream) {
   return entry(ctx, "adamw_step", "mo adamw_step",
-               [&]() { return run_adamw(ctx, of_kind(list, LIST_ADAMW), given(cfg), step, stream); });
+               [&]() { return run_adamw(ctx, of_kind(ctx, list, LIST_ADAMW), given(cfg), step, stream); });
 }
 mo_status adamw8_step_list(mo_ctx* ctx, const mo_list* list, const mo_adamw_cfg* cfg, int64_t step, void* stream) {
   return entry(ctx, "adamw8_step", "mo adamw8_step",
-               [&]() { return run_adamw(ctx, of_kind(list, LIST_ADAMW8), given(cfg), step, stream); });
+               [&]() { return run_adamw(ctx, of_kind(ctx, list, LIST_ADAMW8), given(cfg), step, stream); });
 }
 mo_status adamw8_pack_list(mo_ctx* ctx, const mo_list* list, const mo_pack_cfg* cfg, void* stream) {
   return entry(ctx, "adamw8_pack", "mo adamw8_pack",
-               [&]() { return run_pack(ctx, of_kind(list, LIST_MOMENTS), given(cfg), stream); });
+               [&]() { return run_pack(ctx, of_kind(ctx, list, LIST_MOMENTS), given(cfg), stream); });
 }
 mo_status adamw8_unpack_list(mo_ctx* ctx, const mo_list* list, void* stream) {
   return entry(ctx, "adamw8_unpack", "mo adamw8_unpack",
-               [&]() { return run_unpack(ctx, of_kind(list, LIST_MOMENTS), stream); });
+               [&]() { return run_unpack(ctx, of_kind(ctx, list, LIST_MOMENTS), stream); });
 }
 mo_status clip_grads_list(mo_ctx* ctx, const mo_list* list, const mo_clip_cfg* cfg, void* stream) {
   return entry(ctx, "clip_grads", "mo clip_grads",
-               [&]() { return run_clip(ctx, of_kind(list, LIST_GRADS), given(cfg), stream); });
+               [&]() { return run_clip(ctx, of_kind(ctx, list, LIST_GRADS), given(cfg), stream); });
 }
 
 mo_status adamw_step(mo_ctx* ctx, const mo_adamw_tensor* list, int n, const mo_adamw_cfg* cfg, int64_t step,
                      void* stream) {
   return entry(ctx, "adamw_step", "mo adamw_step", [&]() {
     if (n == 0) return cudaSuccess;
-    return run_adamw(ctx, *build_adamw(list, n), given(cfg), step, stream);
+    return run_adamw(ctx, *build_adamw(ctx, list, n), given(cfg), step, stream);
   });
 }
 mo_status adamw8_step(mo_ctx* ctx, const mo_adamw8_tensor* list, int n, const mo_adamw_cfg* cfg, int64_t step,
                       void* stream) {
   return entry(ctx, "adamw8_step", "mo adamw8_step", [&]() {
     if (n == 0) return cudaSuccess;
-    return run_adamw(ctx, *build_adamw8(list, n), given(cfg), step, stream);
+    return run_adamw(ctx, *build_adamw8(ctx, list, n), given(cfg), step, stream);
   });
 }
 mo_status adamw8_pack(mo_ctx* ctx, const mo_adamw8_moments* list, int n, const mo_pack_cfg* cfg, void* stream) {
   return entry(ctx, "adamw8_pack", "mo adamw8_pack", [&]() {
     if (n == 0) return cudaSuccess;
-    return run_pack(ctx, *build_moments(list, n), given(cfg), stream);
+    return run_pack(ctx, *build_moments(ctx, list, n), given(cfg), stream);
   });
 }
 mo_status adamw8_unpack(mo_ctx* ctx, const mo_adamw8_moments* list, int n, void* stream) {
   return entry(ctx, "adamw8_unpack", "mo adamw8_unpack", [&]() {
     if (n == 0) return cudaSuccess;
-    return run_unpack(ctx, *build_moments(list, n), stream);
+    return run_unpack(ctx, *build_moments(ctx, list, n), stream);
   });
 }
 mo_status clip_grads(mo_ctx* ctx, const mo_grad* list, int n, const mo_clip_cfg* cfg, void* stream) {
   return entry(ctx, "clip_grads", "mo clip_grads",
-               [&]() { return run_clip(ctx, *build_grads(list, n), given(cfg), stream); });
+               [&]() { return run_clip(ctx, *build_grads(ctx, list, n), given(cfg), stream); });
 }
 
 }  // extern "C"

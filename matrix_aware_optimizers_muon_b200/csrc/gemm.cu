@@ -231,9 +231,13 @@ cudaError_t ensure_smem_attr(const void* func, int bytes) {
 }
 
 int device_sm_count() {
-  static int cache[64] = {0};
   int dev = 0;
   cudaGetDevice(&dev);
+  return device_sm_count(dev);
+}
+
+int device_sm_count(int dev) {
+  static int cache[64] = {0};
   if (dev >= 64) return 148;
   if (cache[dev] == 0) {
     int n = 0;

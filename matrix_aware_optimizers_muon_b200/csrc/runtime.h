@@ -155,8 +155,9 @@ struct GemmOp {
 // Launch the tcgen05 GEMM.  Returns cudaSuccess or the launch/encode error.
 cudaError_t launch_gemm(const GemmOp& op, int* status, cudaStream_t stream);
 
-// Number of SMs of the current device (cached per device).
+// Number of SMs of the current device, or of device `dev` (cached per device).
 int device_sm_count();
+int device_sm_count(int dev);
 
 // Round x up to a multiple of a.
 inline long long round_up(long long x, long long a) { return (x + a - 1) / a * a; }
