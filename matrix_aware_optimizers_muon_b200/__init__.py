@@ -125,6 +125,9 @@ class TensorList:
     def __len__(self):
         return len(self.tensors)
 
+    def __reduce__(self):
+        raise TypeError("a TensorList owns a handle of the library and is not copied: make another one")
+
     def __del__(self):
         try:
             self.lib.mo_list_destroy(self.handle)

@@ -1,9 +1,11 @@
 """Refusals and host-side rules of the AdamW, 8-bit-moment and clipping calls
 that test_adamw_abi.py leaves open; none needs a GPU."""
+import copy
 import ctypes
+import pickle
 
 import pytest
-from test_adamw_abi import BAD, _cfg, _step, _tensor, _tensor8, ctx, lib  # noqa: F401
+from test_adamw_abi import BAD, _cfg, _context, _mat, _step, _tensor, _tensor8, ctx, lib  # noqa: F401
 
 from matrix_aware_optimizers_muon_b200 import _lib
 
@@ -59,3 +61,10 @@ def test_a_list_belongs_to_its_contexts_device(lib, ctx):  # noqa: F811
     lib.mo_list_destroy(out)
     for c in (other, same):
         lib.mo_ctx_destroy(c)
+
+
+@pytest.mark.parametrize("how", [copy.copy, copy.deepcopy, pickle.dumps])
+def test_a_list_is_not_copied(lib, how):  # noqa: F811
+    """Two owners of one handle would free it twice."""
+    with pytest.raises(TypeError, match="not copied"):
+        how(_context().adamw_tensors([_mat()]))
