@@ -420,16 +420,18 @@ MO_API mo_status adamw_step(mo_ctx* ctx, const mo_adamw_tensor* list /* host arr
  * With stochastic == 1 both moments take the code above (in magnitude) with the
  * probability of their distance from the one below, from bits that are a function
  * of (seed, step, place in the list, element): their means follow the recurrence.
- * Nearest-even rounding leaves a moment that changes by less than half a code step, 3
- * to 6 % of it, where it is.  V moves by 0.1 % in a step with b2 = 0.999, M by
- * (1 - b1) (g - M): without a gradient and with b1 = 0.95 an M of 9 or 10 eighths of
- * its binade never decays, with b1 = 0.9 the lowest four codes never do, and
- * with a steady one M stops at 0.5 to 0.8 of it.  So do not train with
- * stochastic == 0 (both moments to nearest) for longer than a few steps, nor with 2 (M to
- * nearest, V with noise: M / sqrt(V) grows without bound and W with it), which
- * is there for runs that were begun with it and have to keep their bits.  All zero codes and scales are the
- * zero moments of the first step.  M8 and V8 hold numel bytes, MS and VS
- * ceil(numel / 256).  Everything else is as in adamw_step. */
+ * Nearest-even rounding leaves a moment that changes by less than half a code
+ * step, 3 to 6 % of it, where it is.  V moves by 0.1 % in a step with b2 = 0.999, M
+ * by (1 - b1) (g - M): without a gradient and with b1 = 0.95 an M of 9 or 10
+ * eighths of its binade never decays, with b1 = 0.9 the lowest four codes never do,
+ * and with a steady one M stops at 0.5 to 0.8 of it.  So do not train with
+ * stochastic == 0 (both moments to nearest) for longer than a few steps, nor with
+ * 2 (M to nearest, V with noise: M / sqrt(V) grows without bound and W with it),
+ * which is there for runs that were begun with it and have to keep their bits.
+ * All zero codes and scales are the zero moments of the first step.  M8 and V8
+ * hold numel bytes, MS and VS ceil(numel / 256).  An M within 2^-5 of 2^128 may
+ * take the code of 2^128, which is infinite in fp32.  Everything else is as in
+ * adamw_step. */
 typedef struct {
   int64_t numel;
   void* W;
@@ -493,7 +495,9 @@ MO_API mo_status adamw8_unpack(mo_ctx* ctx, const mo_adamw8_moments* list, int n
  *  - The partial sums are in the attached workspace (MO_CLIP_WORKSPACE_BYTES
  *    at least): like other calls that use it, calls must not overlap on the
  *    GPU while they share one workspace.
- *  - An empty list has norm 0. */
+ *  - An empty list has norm 0.
+ *  - Whether memory overlaps is checked as if apply were 1: a list that names a
+ *    gradient twice is refused with apply == 0 too. */
 #define MO_CLIP_WORKSPACE_BYTES (256u + 8u * 8192u)
 
 typedef struct {
@@ -519,7 +523,8 @@ MO_API mo_status clip_grads(mo_ctx* ctx, const mo_grad* list /* host array */, i
  * The lists of the four kinds of calls above, checked and laid out once: a
  * program whose parameters, gradients and state stay in place makes one and
  * passes it to every step (the checks and tables of 300 tensors take the host
- * some 30 us, a step with a prepared list 4).  A list holds addresses and
+ * some 25 us, a step with a prepared list 4; the Python binding, which checks
+ * every tensor too, some 1000 and 10).  A list holds addresses and
  * sizes, in host memory, and no contents.  A moments list serves adamw8_pack
  * and adamw8_unpack (none of its buffers may overlap another, in the calls with
  * arrays either).  Results and refusals are those of the calls with arrays;

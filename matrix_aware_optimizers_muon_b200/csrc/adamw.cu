@@ -10,15 +10,17 @@
 //
 // What bounds them, and what they reach (218 M elements, one dense layer; 6.54 TB/s
 // is the card's measured copy rate):
-//   fp32 moments, fp32 W, bf16 G and copy   28 B an element   900 us   104 % of it
-//   8-bit moments, bf16 W and G, noise      10 B              390 us    86 %
+//   fp32 moments, fp32 W, bf16 G and copy   28 B an element   901 us   104 % of it
+//   8-bit moments, bf16 W and G, noise      10 B              432 us    77 %
+//       the same, first moment to nearest                     402 us    83 %
+//   8-bit moments, fp32 W, bf16 G, noise    14 B              463 us   101 %
 //   unpack to bf16                           6 B              197 us   102 %
 //   pack from fp32, noise                   10 B              313 us   107 %
-//   norm of bf16 G                           2 B               65 us   102 %
-//   clip bf16 into fp32, G read twice        8 B              273 us    98 %
-// All are bound by HBM but the 8-bit step, which needs 57 instructions an element
-// with bf16 weights and noise, 14 of them for the noise, and keeps the schedulers
-// 85 % busy.
+//   norm of bf16 G                           2 B               67 us    99 %
+//   clip bf16 into fp32, G read twice        8 B              275 us    97 %
+// All are bound by HBM but the 8-bit step of bf16 weights, which needs 67
+// instructions an element (57 with the first moment to nearest) and keeps the
+// schedulers 88 % busy.
 //
 // The moments are formed in fp32 with a fixed order of roundings,
 //   m' = rn(rn(b1 m) + rn((1 - b1) g)),  v' = rn(rn(b2 v) + rn((1 - b2) rn(g g))),
@@ -48,7 +50,9 @@ constexpr int PER = AW_BLOCK / 32;     // elements of a lane
 // CTAs (warps) of a step on one SM, the same number for each of its four
 // schedulers (with one warp more than the others, a scheduler finishes last: 21
 // were as slow as 24 would be).  fp32 moments: 20 at 96 registers, 8 bits and
-// shifted: 28 at 72 (50 M bf16 elements: 99 us; 24: 102, 32: 105).
+// shifted: 28 at 72 (50 M bf16 elements: 99 us; 24: 102, 32: 105).  At these limits
+// ptxas spills 8 to 36 bytes of the fp32 step with bf16 weights or fp32
+// gradients, 8 of some shifted 8-bit ones and none of the aligned 8-bit step.
 constexpr int STEP32_CTAS = 20;
 constexpr int STEP8_CTAS = 28;
 
@@ -504,7 +508,9 @@ struct Noise {
     return n;
   }
   // Element j's 16 bits; and those with a half behind them in bits 7 to 23.  By
-  // shifts and masks: where byte permutations made them, nvcc 12.9 lost v's code.
+  // shifts and masks: made by byte permutations and packed by pack_tops they gave every v
+  // of pack_kernel the code 1 (nvcc 12.9; why was not found).  The tests compare
+  // the codes of this form bit for bit with the oracle's.
   __device__ __forceinline__ unsigned bits16(int j) const {
     return (WIDE ? j : threadIdx.x) % 2 ? w[WIDE ? j / 2 : j] >> 16 : w[WIDE ? j / 2 : j] & 0xffffu;
   }
@@ -532,8 +538,8 @@ struct Noise {
 // subnormals included, and what is rounded off below them; times
 // 2^(127 - s) 2^-120 it has m's in bits 20 to 26, below its sign.  Noise is added
 // there (16 bits and a half behind them), which is unbiased to 2^-17 of a code step.
-// m's noise costs the step of 50 M elements 11 us with bf16 weights (108; v's alone
-// 98, none 87) and nothing with fp32 ones (114), where HBM is the bound.
+// m's noise costs the step of 50 M elements 7 us with bf16 weights (106; v's alone
+// 99, none 87) and nothing with fp32 ones (114), where HBM is the bound.
 constexpr unsigned INF_BITS = 0x7f800000u;
 constexpr unsigned HIGH_BITS = 0x4e000000u;   // 2^29: below, v's scale is at most 2^14
 constexpr unsigned FIRST_HIGH_BITS = 0x46000000u;   // 2^13: below, m's scale is at most 2^5
