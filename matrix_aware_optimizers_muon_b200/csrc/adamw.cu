@@ -509,8 +509,8 @@ struct Noise {
   }
   // Element j's 16 bits; and those with a half behind them in bits 7 to 23.  By
   // shifts and masks: made by byte permutations and packed by pack_tops they gave every v
-  // of pack_kernel the code 1 (nvcc 12.9; why was not found).  The tests compare
-  // the codes of this form bit for bit with the oracle's.
+  // of pack_kernel the code 1 (nvcc 12.9; why was not found).  The tests hold
+  // the codes of this form to those of the definition, bit for bit.
   __device__ __forceinline__ unsigned bits16(int j) const {
     return (WIDE ? j : threadIdx.x) % 2 ? w[WIDE ? j / 2 : j] >> 16 : w[WIDE ? j / 2 : j] & 0xffffu;
   }
