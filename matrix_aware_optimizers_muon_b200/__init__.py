@@ -539,26 +539,27 @@ class Context:
                     bias_correction, grad_scale, skip, seed is not None, seed, stream)
 
     @staticmethod
-    def _rounding(noise, default, seed):
+    def _rounding(noise, seed, default):
         """The library's kind of rounding of an 8-bit call, and its seed."""
-        if seed is not _NOT_GIVEN and noise != default:
-            raise ValueError("noise and seed are two kinds of rounding: give one of them")
         if seed is _NOT_GIVEN:
+            noise = default if noise is _NOT_GIVEN else noise
             return int(noise is not None), noise
+        if noise is not _NOT_GIVEN:
+            raise ValueError("noise and seed are two kinds of rounding: give one of them")
         return 2 * (seed is not None), seed
 
     def adamw8_step(self, mats, step, *, lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, bias_correction=True,
-                    grad_scale=None, skip=None, noise=0, seed=_NOT_GIVEN, stream=None):
+                    grad_scale=None, skip=None, noise=_NOT_GIVEN, seed=_NOT_GIVEN, stream=None):
         """One AdamW step with both moments in 8 bits (adamw8_tensors, or what
-        it takes).  ``noise`` is the seed with which both moments and bf16 weights
-        are rounded stochastically; None rounds to nearest, which leaves moments
+        it takes).  ``noise`` (0) is the seed with which both moments and bf16
+        weights are rounded stochastically; None rounds to nearest, which leaves moments
         that change by less than half a code step where they are: over more than
         a few steps the first no longer follows the gradient.
 
         ``seed`` in place of ``noise`` is an earlier form, for runs that have to
         keep its bits: the first moment is rounded to nearest and sticks to its code
         while the second decays, so that weights without gradient run away."""
-        stochastic, seed = self._rounding(noise, 0, seed)
+        stochastic, seed = self._rounding(noise, seed, 0)
         if stochastic == 2 and not Context._warned:
             Context._warned = True
             warnings.warn("adamw8_step(seed=...) rounds the first moment to the nearest code, where it sticks: "
@@ -566,12 +567,12 @@ class Context:
         self._adamw(self.lib.adamw8_step_list, self._list("adamw8", mats), step, lr, beta1, beta2, eps,
                     bias_correction, grad_scale, skip, stochastic, seed, stream)
 
-    def adamw8_pack(self, mats, *, noise=None, seed=None, step=0, stream=None):
-        """Moments M, V to 8-bit codes (adamw8_moments, or what it takes); with
-        ``noise`` both are rounded stochastically, with ``seed`` V alone, with the bits
-        of ``step``."""
+    def adamw8_pack(self, mats, *, noise=_NOT_GIVEN, seed=_NOT_GIVEN, step=0, stream=None):
+        """Moments M, V to 8-bit codes (adamw8_moments, or what it takes), to
+        nearest; with ``noise`` both are rounded stochastically, with ``seed`` V
+        alone, with the bits of ``step``."""
         torch = self._torch
-        stochastic, seed = self._rounding(noise, None, _NOT_GIVEN if seed is None else seed)
+        stochastic, seed = self._rounding(noise, seed, None)
         mats = self._list("moments", mats)
         step_dev = None
         if isinstance(step, torch.Tensor):

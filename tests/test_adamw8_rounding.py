@@ -51,3 +51,13 @@ def test_pack(calls):
     assert seen == [(0, 0), (1, 0), (2, 0), (1, 3), (2, 3)]
     with pytest.raises(ValueError, match="noise and seed"):
         c.adamw8_pack(lst, noise=1, seed=1)
+
+
+def test_both_given(calls):
+    """A noise of 0 that the caller wrote is not the default: with seed=None beside it the call would not know which is meant."""
+    c, seen = calls
+    lst = c.adamw8_tensors([_mat8()])
+    for kw in (dict(noise=0, seed=None), dict(noise=0, seed=0), dict(noise=None, seed=None)):
+        with pytest.raises(ValueError, match="noise and seed"):
+            c.adamw8_step(lst, 1, **kw)
+    assert not seen
